@@ -481,6 +481,150 @@ nvfp4_status nvfp4_moe_fc1_f16(const void* x, int64_t ld_x, int64_t T, const int
                                const float* global_scales, int global_scale_is_divisor, int activation, void* a,
                                int64_t ld_a, int64_t R, int64_t E, int64_t I, int64_t K, void* stream);
 
+/* ---- The attention half of a decoder layer -----------------------------------
+ *
+ * What a decoder layer runs around its FP4 linears when it serves one new
+ * token per sequence (or writes a prompt's tokens into its cache): the norm
+ * with the residual's addition, rotary positions, the paged key-value cache
+ * and the attention over it.  f16 selects fp16 activations (0: bf16); every
+ * 16-bit array of a call has that type.  Strides are in elements of the array
+ * unless a byte stride is named.  All rows start 16-byte aligned and are
+ * contiguous, except where stated. */
+
+/* Root-mean-square norm.  Row t of T, N values:
+ *   h = residual ? RNE16(x + residual) : x          (stored to h if given)
+ *   v = h * rsqrt(mean(h^2) + eps) * weight         (fp32, over h as rounded)
+ *   scales == NULL: y[t] = RNE16(v);
+ *   scales != NULL: y[t] = e4m3(v * fp32(1 / s)), scales[t] = s = max(fp32(max |v| / 448), 2^-126)
+ *                   (bytes; the value a byte stands for is e4m3 * s).
+ *   x [T][ld_x], residual [T][ld_r] or NULL, weight [N], y [T][ld_y] of 16-bit
+ *   values or bytes, scales fp32 [T] or NULL, h [T][ld_h] or NULL (needs a
+ *   residual).  h may be residual's or x's memory with the same leading
+ *   dimension, and y x's if it is 16 bits wide and h does not take it; no other
+ *   overlap.  2-byte alignment of rows suffices (1-byte for 8-bit y, 4-byte
+ *   for scales); rows and leading dimensions of 16 bytes (8 for 8-bit y) and N
+ *   a multiple of 8 up to 32768 take the one-pass kernel.
+ * T == 0 launches nothing.  Errors: T < 0 or T >= 2^31, N < 1 or N >= 2^31, a leading dimension < N, eps
+ * negative or not finite, h without residual, NULL x / weight / y -> INVALID_ARG; misaligned -> ALIGNMENT. */
+nvfp4_status nvfp4_rms_norm(const void* x, int64_t ld_x, const void* residual, int64_t ld_r, const void* weight,
+                            float eps, void* y, int64_t ld_y, float* scales, void* h, int64_t ld_h, int64_t T,
+                            int64_t N, int f16, void* stream);
+
+/* Rotary positions.  The first R columns of each head are turned in R / 2
+ * pairs, columns (i, i + R / 2), or (2 i, 2 i + 1) with neighbours; the rest
+ * pass.  Pair i of token t turns by
+ *   angle = positions[axis(i)][t] * inv_freq[i]     (in 64 bits),
+ *   (x0, x1) -> RNE16(x0 c - x1 s), RNE16(x1 c + x0 s),
+ * c and s the cosine and sine rounded to fp32, each product and sum rounded to
+ * fp32.  axis(i) = pair_axis[i], or 0 with pair_axis NULL; several axes serve
+ * positions of images and video (time, height, width).
+ *   inv_freq fp32 [R / 2]; positions int32 [axes][ld_pos], negative ones too;
+ *   pair_axis int32 [R / 2] or NULL (values outside [0, axes) are clamped). */
+typedef struct {
+    const float* inv_freq;
+    const int32_t* positions;
+    const int32_t* pair_axis;
+    int64_t ld_pos;
+    int32_t axes;
+    int32_t rotary;      /* R: even columns turned, a multiple of 16 */
+    int32_t neighbours;  /* pairs (2 i, 2 i + 1) instead of (i, i + R / 2) */
+    int32_t reserved;    /* 0 */
+} nvfp4_rope;
+
+/* The paged key-value cache: `pages` pages of `page_size` tokens, `heads`
+ * key-value heads of head_dim = D columns.  The block of a (page, head) starts
+ * at page * stride[0] + head * stride[1] bytes:
+ *   NVFP4_KV_16BIT  values of the activation type, row i of the page stride[2]
+ *                   bytes after row i - 1; no scales;
+ *   NVFP4_KV_E4M3   E4M3 bytes, rows likewise; the stored value of x in head h
+ *                   is e4m3(sat448(fp32(x * fp32(1 / scale[h]))));
+ *   NVFP4_KV_NVFP4  page_size * D / 2 code bytes (token-major, two E2M1 codes a
+ *                   byte, the even column in the low nibble), then page_size *
+ *                   D / 16 E4M3 group scales (token-major, one per 16 columns);
+ *                   stride[2] is not used.  A group with the largest absolute
+ *                   value a gets the scale S = e4m3(sat448(fp32(fp32(a * r) *
+ *                   fp32(1 / 6)))), r = fp32(1 / scale[h]), and the codes
+ *                   e2m1(sat6(fp32(x * fp32(r / S)))), all 0 where S is 0.  A
+ *                   NaN in the group makes S and so the group NaN.
+ * Values read back as code (* S) * scale[h].  Roundings are to nearest, ties to
+ * even.  k_scale / v_scale: device fp32 [heads], positive, or NULL for 1 (must
+ * be NULL for NVFP4_KV_16BIT).
+ * D: a multiple of 16 in [16, 256] (of 32 for NVFP4_KV_NVFP4); page_size >= 1,
+ * any size (NVFP4: page_size * 9 * D / 16 a multiple of 16); strides multiples
+ * of 16 bytes, non-negative; at most 64 GB from the first to the last block of
+ * each side; pages * page_size < 2^31. */
+enum { NVFP4_KV_16BIT = 0, NVFP4_KV_E4M3 = 1, NVFP4_KV_NVFP4 = 2 };
+typedef struct {
+    void* k;
+    void* v;
+    const float* k_scale;
+    const float* v_scale;
+    int64_t k_stride[3];   /* bytes: page, head, token */
+    int64_t v_stride[3];
+    int64_t pages;
+    int32_t page_size;
+    int32_t heads;
+    int32_t head_dim;
+    int32_t format;
+} nvfp4_kv_cache;
+
+/* Rotates x [T][H][D] (strides x_t, x_h) into out (strides o_t, o_h), which may
+ * be x itself with the same strides.  D a multiple of 16 in [16, 1024], R <=
+ * min(D, 256).  T == 0 or H == 0 launches nothing.  Errors: sizes, NULL
+ * pointers -> INVALID_ARG; rows or strides not multiples of 16 bytes,
+ * misaligned arrays -> ALIGNMENT. */
+nvfp4_status nvfp4_rope_apply(const nvfp4_rope* rope, const void* x, int64_t x_t, int64_t x_h, void* out, int64_t o_t,
+                              int64_t o_h, int64_t T, int64_t H, int64_t D, int f16, void* stream);
+
+/* Appends T tokens to the cache: keys k [T][heads][D] (strides k_t, k_h) and
+ * values v go to row slots[t] % page_size of page slots[t] / page_size; tokens
+ * whose slot is negative or past the cache are skipped (padding).  Two tokens
+ * with one slot leave either one's row.  With rope the keys are rotated first
+ * and rounded to 16 bits (R a multiple of 32 for NVFP4_KV_NVFP4, at most 256),
+ * and queries q [T][Hq][D] are rotated into q_out in the same launch, padding
+ * included (q_out may be q; Hq = 0 and NULL without queries).
+ * Errors as above, plus an invalid cache description -> INVALID_ARG /
+ * ALIGNMENT, queries without rope -> INVALID_ARG. */
+nvfp4_status nvfp4_kv_append(const nvfp4_kv_cache* cache, const nvfp4_rope* rope, const void* q, int64_t q_t,
+                             int64_t q_h, void* q_out, int64_t qo_t, int64_t qo_h, int64_t Hq, const void* k,
+                             int64_t k_t, int64_t k_h, const void* v, int64_t v_t, int64_t v_h, const int32_t* slots,
+                             int64_t T, int f16, void* stream);
+
+/* Reads rows back in 16 bits: k[t] and v[t] (16-bit [T][heads][D]) = RNE16 of
+ * the values of slot slots[t], zeros for a slot outside the cache. */
+nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const int32_t* slots, void* k, int64_t k_t, int64_t k_h,
+                           void* v, int64_t v_t, int64_t v_h, int64_t T, int f16, void* stream);
+
+/* Attention of one new token per sequence.  Sequence b of B has lengths[b]
+ * cached tokens (the new one's own key and value among them); token t is row
+ * t % page_size of page page_table[b][t / page_size].  Query head j reads
+ * key-value head j / (Hq / heads):
+ *   w_t = exp(softmax_scale * q . k_t),  t in [max(0, L - window), L)
+ *   out = sum_t w_t v_t / sum_t w_t,     lse = ln sum_t w_t
+ * (window 0: every token).  With no tokens, or only tokens of weight 0, out is
+ * 0 and lse -inf.  Lengths are clamped to [0, max_pages * page_size]; the
+ * tokens of a page whose table entry is outside [0, pages) are left out.
+ *   q [B][Hq][D] and out [B][Hq][D] of the activation type (strides q_b, q_h,
+ *   o_b, o_h; out may be q with the same strides), lse fp32 [B][Hq] or NULL, page_table int32
+ *   [B][ld_table] (max_pages entries used), lengths int32 [B].
+ * Products are fp32-accumulated MFMAs on bf16 (bf16 cache) or fp16 values;
+ * softmax statistics and sums are fp32; results are bitwise reproducible.
+ *   workspace: nvfp4_paged_attention_workspace_bytes(B, Hq, heads, D,
+ *   max_pages * page_size) bytes, 256-byte aligned, zero-filled before its first
+ *   use; every call leaves the counters in it zero, so one workspace serves any
+ *   number of calls of any sizes one after another (not calls that may overlap
+ *   in time, and not the GEMMs: theirs has another layout).
+ * B == 0 launches nothing.  Errors: sizes, B > 65535, heads * ceil(Hq / heads / 16) >
+ * 65535, Hq not a multiple of heads, max_pages < 0, max_pages * page_size >=
+ * 2^30, softmax_scale not finite, window < 0, NULL pointers -> INVALID_ARG;
+ * misaligned -> ALIGNMENT; workspace too small -> BUFFER_TOO_SMALL. */
+int64_t nvfp4_paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t heads, int64_t D, int64_t max_tokens);
+nvfp4_status nvfp4_paged_attention(const nvfp4_kv_cache* cache, const void* q, int64_t q_b, int64_t q_h,
+                                   const int32_t* page_table, int64_t ld_table, int64_t max_pages,
+                                   const int32_t* lengths, int64_t B, int64_t Hq, float softmax_scale, int64_t window,
+                                   void* out, int64_t o_b, int64_t o_h, float* lse, void* workspace,
+                                   int64_t workspace_bytes, int f16, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

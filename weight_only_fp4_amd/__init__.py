@@ -25,7 +25,9 @@ __all__ = ["repack", "repack_bytes", "gemm", "gemm_variant", "grouped_gemm", "de
            "moe_combine",
            "gemm_plan", "gemm_variants", "gemm_noalloc", "stream_read", "repack_mxfp4", "dequant_mxfp4",
            "gemm_mxfp4", "gemm_variant_mxfp4", "grouped_gemm_mxfp4", "VARIANT_AUTO", "VARIANT_SMALL_M", "VARIANT_LARGE_M", "VARIANT_MFMA", "VARIANT_RESIDENT",
-           "VARIANT_MFMA_QUARTER", "VARIANT_KERNELS", "LIB_PATH"]
+           "VARIANT_MFMA_QUARTER", "VARIANT_KERNELS", "LIB_PATH",
+           "rms_norm", "rms_norm_fp8", "rope", "rope_pair_axis", "kv_cache", "kv_write", "rope_kv_write", "kv_read",
+           "paged_attention", "paged_attention_workspace_bytes"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnvfp4_w4a16.so")
 VARIANT_AUTO, VARIANT_SMALL_M, VARIANT_LARGE_M, VARIANT_MFMA, VARIANT_RESIDENT = 0, 1, 2, 3, 4
@@ -118,6 +120,21 @@ def lib() -> ctypes.CDLL:
         L.nvfp4_w4a16_grouped_gemm_variant.argtypes = [P, I64, I64, P, P, P, P, P, I, I, P, I64, I64, I64, I64, I64,
                                                        I, I, I, P]
         L.nvfp4_w4a16_grouped_gemm_variant.restype = I
+        F, DESC = ctypes.c_float, ctypes.c_char_p   # DESC: a packed descriptor (nvfp4_rope, nvfp4_kv_cache)
+        L.nvfp4_rms_norm.argtypes = [P, I64, P, I64, P, F, P, I64, P, P, I64, I64, I64, I, P]
+        L.nvfp4_rms_norm.restype = I
+        L.nvfp4_rope_apply.argtypes = [DESC, P, I64, I64, P, I64, I64, I64, I64, I64, I, P]
+        L.nvfp4_rope_apply.restype = I
+        L.nvfp4_kv_append.argtypes = [DESC, DESC, P, I64, I64, P, I64, I64, I64, P, I64, I64, P, I64, I64, P, I64, I,
+                                      P]
+        L.nvfp4_kv_append.restype = I
+        L.nvfp4_kv_read.argtypes = [DESC, P, P, I64, I64, P, I64, I64, I64, I, P]
+        L.nvfp4_kv_read.restype = I
+        L.nvfp4_paged_attention_workspace_bytes.argtypes = [I64, I64, I64, I64, I64]
+        L.nvfp4_paged_attention_workspace_bytes.restype = I64
+        L.nvfp4_paged_attention.argtypes = [DESC, P, I64, I64, P, I64, I64, P, I64, I64, F, I64, P, I64, I64, P, P,
+                                            I64, I, P]
+        L.nvfp4_paged_attention.restype = I
         _lib = L
     return _lib
 
@@ -582,3 +599,7 @@ def moe_combine(y, token_row, topk_weights, out=None):
     _check(fn(_ptr(y), y.stride(0), _ptr(token_row), _ptr(topk_weights), T, k, H, _ptr(out), out.stride(0),
               _stream(y.device)))
     return out
+
+
+from .attention import (kv_cache, kv_read, kv_write, paged_attention, paged_attention_workspace_bytes,  # noqa: E402
+                        rms_norm, rms_norm_fp8, rope, rope_kv_write, rope_pair_axis)

@@ -35,6 +35,10 @@ VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]   # MFMA results in VGPRs (post
 SOURCES = [
     ("nvfp4_w4a16.hip", VGPR_FORM, "abi"),
     ("nvfp4_mfma.hip", [], "mfma_plan"),
+    ("nvfp4_attention.hip", VGPR_FORM, "attention"),
+] + [
+    # single-token attention, one unit per cache format (bf16, fp16, E4M3, NVFP4)
+    ("attn.hip", VGPR_FORM + [f"-DNVFP4_KV_FMT={fmt}"], f"attn_{fmt}") for fmt in range(4)
 ] + [
     (f"gemm_{fam}.hip", VGPR_FORM + [f"-DNVFP4_ACT_F16={f16}"], f"{fam}_{f16}")
     for fam in ("small", "tile") for f16 in (0, 1)

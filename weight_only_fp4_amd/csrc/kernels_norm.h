@@ -1,0 +1,183 @@
+// Root-mean-square norm of rows, with the residual's addition before it and
+// an output in 16 or 8 bits.
+#pragma once
+#include "decode.h"
+#include "quant.h"
+
+namespace nvfp4 {
+
+// Row t of N values:
+//   h = RNE16(x + r)  (h = x without a residual; h is stored when asked for),
+//   y = h * rsqrt(mean(h^2) + eps) * w                    (fp32),
+//   out = RNE16(y), or with F8 out = e4m3(y * (1 / s)), s = max(max |y| / 448, 2^-126).
+// The mean is taken over h as it is stored, so the fused call gives what an
+// addition in 16 bits followed by a norm gives.  Sums are fp32 in a fixed
+// order (lanes, then waves), so results are reproducible.
+struct NormArgs {
+    const uint16_t *x, *r, *w;
+    uint16_t* h;
+    void* y;
+    float* scales;
+    int64_t ld_x, ld_r, ld_h, ld_y;
+    int64_t T;
+    int N;
+    float eps;
+};
+
+constexpr int kNormMaxWaves = 16;
+
+// Sum over the wave (every lane gets it): five DPP-free shuffles.
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+    return v;
+}
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) {
+        const uint32_t o = __shfl_xor(v, d);
+        v = o > v ? o : v;
+    }
+    return v;
+}
+
+// One workgroup per row, the row held in registers (V 16-byte pieces a
+// thread): one pass over HBM.  N, the leading dimensions and the pointers
+// keep 16-byte alignment (checked on the host).
+template <bool F16, bool F8, int V>
+__global__ void __launch_bounds__(64 * kNormMaxWaves) k_rms_norm(NormArgs a) {
+    __shared__ float s_sum[kNormMaxWaves];
+    __shared__ uint32_t s_max[kNormMaxWaves];
+    const int tid = threadIdx.x, threads = blockDim.x, waves = threads >> 6;
+    const int64_t t = blockIdx.x;
+    const int pieces = a.N >> 3;
+    float f[V][8];
+    float sum = 0.f;
+    uint4 xv[V], rv[V], wv[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int p = tid + i * threads;
+        if (p < pieces) {
+            xv[i] = *reinterpret_cast<const uint4*>(a.x + t * a.ld_x + p * 8);
+            if (a.r) rv[i] = *reinterpret_cast<const uint4*>(a.r + t * a.ld_r + p * 8);
+            wv[i] = *reinterpret_cast<const uint4*>(a.w + p * 8);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int p = tid + i * threads;
+        if (p < pieces) {
+            unpack8<F16>(xv[i], f[i]);
+            if (a.r) {
+                float rf[8];
+                unpack8<F16>(rv[i], rf);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[i][e] += rf[e];
+                const uint4 h = pack8<F16>(f[i]);
+                if (a.h) *reinterpret_cast<uint4*>(a.h + t * a.ld_h + p * 8) = h;
+                unpack8<F16>(h, f[i]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(f[i][e], f[i][e], sum);
+        }
+    }
+    sum = wave_sum(sum);
+    if (waves > 1) {
+        if ((tid & 63) == 0) s_sum[tid >> 6] = sum;
+        __syncthreads();
+        sum = 0.f;
+        for (int i = 0; i < waves; ++i) sum += s_sum[i];
+    }
+    const float inv = rsqrtf(sum / (float)a.N + a.eps);
+    uint32_t top = 0u;   // largest |y| as bits: a NaN's are above infinity's, so it is kept
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int p = tid + i * threads;
+        if (p < pieces) {
+            float wf[8];
+            unpack8<F16>(wv[i], wf);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                f[i][e] = f[i][e] * inv * wf[e];
+                if constexpr (F8) {
+                    const uint32_t u = __float_as_uint(f[i][e]) & 0x7FFFFFFFu;
+                    top = u > top ? u : top;
+                }
+            }
+            if constexpr (!F8)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + t * a.ld_y + p * 8) = pack8<F16>(f[i]);
+        }
+    }
+    if constexpr (F8) {
+        top = wave_max_u32(top);
+        if (waves > 1) {
+            if ((tid & 63) == 0) s_max[tid >> 6] = top;
+            __syncthreads();
+            for (int i = 0; i < waves; ++i) top = s_max[i] > top ? s_max[i] : top;
+        }
+        const float scale = norm_row_scale(__uint_as_float(top));
+        const float back = __fdiv_rn(1.0f, scale);
+        if (tid == 0) a.scales[t] = scale;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int p = tid + i * threads;
+            if (p < pieces)
+                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + t * a.ld_y + p * 8) = e4m3_pack8(f[i], back);
+        }
+    }
+}
+
+// Any row length, stride and alignment: one workgroup of 256 threads per row,
+// single values, the row read again for each of the two or three passes.
+// With h the later passes read h back (each thread its own values), so h may
+// be the residual's or x's own memory; y is written in the last pass only.
+template <bool F16, bool F8>
+__global__ void __launch_bounds__(256) k_rms_norm_any(NormArgs a) {
+    __shared__ float s_sum[4];
+    __shared__ uint32_t s_max[4];
+    const int tid = threadIdx.x;
+    const int64_t t = blockIdx.x;
+    const uint16_t* x = a.x + t * a.ld_x;
+    const uint16_t* r = a.r ? a.r + t * a.ld_r : nullptr;
+    uint16_t* h = a.h ? a.h + t * a.ld_h : nullptr;
+    const bool again = r != nullptr && h != nullptr;
+    float sum = 0.f;
+    for (int i = tid; i < a.N; i += 256) {
+        uint32_t v = x[i];
+        if (r) v = round_out<F16>(act_to_f32<F16>(v) + act_to_f32<F16>(r[i]));
+        if (again) h[i] = (uint16_t)v;
+        const float f = act_to_f32<F16>(v);
+        sum = __builtin_fmaf(f, f, sum);
+    }
+    sum = wave_sum(sum);
+    if ((tid & 63) == 0) s_sum[tid >> 6] = sum;
+    __syncthreads();
+    sum = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+    const float inv = rsqrtf(sum / (float)a.N + a.eps);
+    auto value = [&](int i) {
+        uint32_t v = again ? h[i] : x[i];
+        if (r && !again) v = round_out<F16>(act_to_f32<F16>(v) + act_to_f32<F16>(r[i]));
+        return act_to_f32<F16>(v) * inv * act_to_f32<F16>(a.w[i]);
+    };
+    if constexpr (!F8) {
+        uint16_t* y = static_cast<uint16_t*>(a.y) + t * a.ld_y;
+        for (int i = tid; i < a.N; i += 256) y[i] = (uint16_t)round_out<F16>(fp32_value(value(i)));
+    } else {
+        uint32_t top = 0u;
+        for (int i = tid; i < a.N; i += 256) {
+            const uint32_t u = __float_as_uint(value(i)) & 0x7FFFFFFFu;
+            top = u > top ? u : top;
+        }
+        top = wave_max_u32(top);
+        if ((tid & 63) == 0) s_max[tid >> 6] = top;
+        __syncthreads();
+        for (int i = 0; i < 4; ++i) top = s_max[i] > top ? s_max[i] : top;
+        const float scale = norm_row_scale(__uint_as_float(top));
+        const float back = __fdiv_rn(1.0f, scale);
+        if (tid == 0) a.scales[t] = scale;
+        uint8_t* y = static_cast<uint8_t*>(a.y) + t * a.ld_y;
+        for (int i = tid; i < a.N; i += 256) y[i] = (uint8_t)e4m3_byte(value(i) * back);
+    }
+}
+
+}  // namespace nvfp4
