@@ -10,12 +10,19 @@ namespace nvfp4 {
 
 namespace {
 
-template <int DT, bool FULL>
-void launch(const AttnArgs& a, int64_t B, int64_t Hk, hipStream_t st) {
+template <int DT, bool FAST>
+void launch(const AttnArgs& a, int64_t workgroups, hipStream_t st) {
     const int nh = a.G < kAttnHeads ? a.G : kAttnHeads;
-    const size_t lds = (size_t)kAttnWaves * nh * (DT / attn_out_passes(DT) + 4) * sizeof(float);
-    const dim3 grid((unsigned)a.S, (unsigned)(Hk * a.head_tiles), (unsigned)B);
-    hipLaunchKernelGGL((k_paged_attn<NVFP4_KV_FMT, DT, FULL>), grid, dim3(kAttnWaves * 64), lds, st, a);
+    const size_t out = (size_t)kAttnWaves * nh * (kAttnOutCols + 4) * sizeof(float);
+    const size_t join = (size_t)kAttnMaxWorkgroups * nh * sizeof(float);   // factors of every partial result
+    hipLaunchKernelGGL((k_paged_attn<NVFP4_KV_FMT, DT, FAST>), dim3((unsigned)workgroups), dim3(kAttnThreads),
+                       out > join ? out : join, st, a);
+}
+
+template <int DT>
+void launch_dt(const AttnArgs& a, bool fast, int64_t workgroups, hipStream_t st) {
+    if (fast && a.shape.D == DT) launch<DT, true>(a, workgroups, st);
+    else launch<DT, false>(a, workgroups, st);
 }
 
 }  // namespace
@@ -30,14 +37,10 @@ void launch(const AttnArgs& a, int64_t B, int64_t Hk, hipStream_t st) {
 #define NVFP4_ATTN_LAUNCHER launch_attn_nvfp4
 #endif
 
-void NVFP4_ATTN_LAUNCHER(const AttnArgs& a, int64_t B, int64_t Hk, hipStream_t st) {
-    const int D = a.shape.D;
-    if (D == 64) launch<64, true>(a, B, Hk, st);
-    else if (D < 64) launch<64, false>(a, B, Hk, st);
-    else if (D == 128) launch<128, true>(a, B, Hk, st);
-    else if (D < 128) launch<128, false>(a, B, Hk, st);
-    else if (D == 256) launch<256, true>(a, B, Hk, st);
-    else launch<256, false>(a, B, Hk, st);
+void NVFP4_ATTN_LAUNCHER(const AttnArgs& a, bool fast, int64_t workgroups, hipStream_t st) {
+    if (a.shape.D <= 64) launch_dt<64>(a, fast, workgroups, st);
+    else if (a.shape.D <= 128) launch_dt<128>(a, fast, workgroups, st);
+    else launch_dt<256>(a, fast, workgroups, st);
 }
 
 }  // namespace nvfp4

@@ -35,6 +35,7 @@ void launch_norm(const NormArgs& a, bool vec, hipStream_t st) {
     else hipLaunchKernelGGL((k_rms_norm<F16, F8, 4>), grid, dim3(threads), 0, st, a);
 }
 
+constexpr int64_t kAttnWorkgroups = 256;   // of a split call: one per compute unit
 constexpr int64_t kNormVecMax = 1024 * 8 * 4;
 
 // ------------------------------------------------------------ cache checks --
@@ -333,7 +334,7 @@ extern "C" {
 
 int64_t nvfp4_paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t heads, int64_t D, int64_t max_tokens) {
     if (check_attn_sizes("nvfp4_paged_attention_workspace_bytes", B, Hq, heads, D, max_tokens) != NVFP4_OK) return -1;
-    return attn_shape(B, heads, Hq / heads, D, max_tokens).total;
+    return attn_shape(B, heads, Hq / heads, D, max_tokens, kAttnMaxWorkgroups).total;
 }
 
 nvfp4_status nvfp4_paged_attention(const nvfp4_kv_cache* cache, const void* q, int64_t q_b, int64_t q_h,
@@ -360,15 +361,13 @@ nvfp4_status nvfp4_paged_attention(const nvfp4_kv_cache* cache, const void* q, i
     if (!aligned(page_table, 4) || !aligned(lengths, 4) || !aligned(lse, 4))
         return fail(NVFP4_ERR_ALIGNMENT, "%s: page_table, lengths and lse must be 4-byte aligned", fn);
     const int64_t G = Hq / c.shape.heads;
-    const int64_t seen = window > 0 && window < max_tokens ? window : max_tokens;
-    const AttnShape full = attn_shape(B, c.shape.heads, G, c.shape.D, max_tokens);
-    if (full.total > 0) {
-        if (!workspace || workspace_bytes < full.total)
+    const AttnShape sh = attn_shape(B, c.shape.heads, G, c.shape.D, max_tokens, kAttnWorkgroups);
+    if (sh.total > 0) {
+        if (!workspace || workspace_bytes < sh.total)
             return fail(NVFP4_ERR_BUFFER_TOO_SMALL, "%s: workspace of %lld bytes is below the %lld bytes this call needs", fn,
-                        (long long)workspace_bytes, (long long)full.total);
+                        (long long)workspace_bytes, (long long)sh.total);
         if (!aligned(workspace, 256)) return fail(NVFP4_ERR_ALIGNMENT, "%s: workspace must be 256-byte aligned", fn);
     }
-    const AttnShape sh = attn_shape(B, c.shape.heads, G, c.shape.D, seen);
     AttnArgs a;
     a.q = static_cast<const uint16_t*>(q);
     a.q_b = q_b;
@@ -390,14 +389,23 @@ nvfp4_status nvfp4_paged_attention(const nvfp4_kv_cache* cache, const void* q, i
     a.o_h = o_h;
     a.lse = lse;
     a.f16 = f16 != 0;
-    a.S = sh.S;
+    a.split = sh.split;
+    a.B = (int)B;
     a.counters = static_cast<int*>(workspace);
     a.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAttnCounterBytes);
     hipStream_t st = static_cast<hipStream_t>(stream);
-    if (c.format == kKvE4m3) launch_attn_e4m3(a, B, c.shape.heads, st);
-    else if (c.format == kKvNvfp4) launch_attn_nvfp4(a, B, c.shape.heads, st);
-    else if (f16) launch_attn_f16(a, B, c.shape.heads, st);
-    else launch_attn_bf16(a, B, c.shape.heads, st);
+    // umulhi(t, ceil(2^(32 + s) / page_size)) >> s is t / page_size for t < 2^31 with 2^s < page_size <= 2^(s + 1)
+    a.page_shift = 0;
+    while ((int64_t)2 << a.page_shift < c.shape.page_size) ++a.page_shift;
+    a.page_magic = c.shape.page_size == 1 ? 0u
+                   : (uint32_t)((((uint64_t)1 << (32 + a.page_shift)) + c.shape.page_size - 1) / (uint64_t)c.shape.page_size);
+    // 32-bit offsets inside a half-tile of 16 tokens
+    const int64_t far = (int64_t)1 << 26;
+    const bool fast = c.shape.page_size % 16 == 0 && (c.format == kKvNvfp4 || (c.k.s_token < far && c.v.s_token < far));
+    if (c.format == kKvE4m3) launch_attn_e4m3(a, fast, sh.workgroups, st);
+    else if (c.format == kKvNvfp4) launch_attn_nvfp4(a, fast, sh.workgroups, st);
+    else if (f16) launch_attn_f16(a, fast, sh.workgroups, st);
+    else launch_attn_bf16(a, fast, sh.workgroups, st);
     return launched(fn);
 }
 
