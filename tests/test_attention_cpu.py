@@ -2,6 +2,7 @@
 fake), the binding's checks, workspace sizes, and the plain forms the GPU tests compare with."""
 import ctypes
 import math
+import struct
 
 import numpy as np
 import pytest
@@ -9,10 +10,35 @@ import torch
 
 import attention_ref as ref
 import weight_only_fp4_amd as nv
-from weight_only_fp4_amd import attention as at
 
 OK, INVALID, ALIGN, SMALL = 0, 1, 2, 3
 A = 1 << 20   # a fake, aligned address; never dereferenced
+
+
+# the C structs nvfp4_kv_cache and nvfp4_rope
+KV_STRUCT, ROPE_STRUCT = struct.Struct("PPPP7q4i"), struct.Struct("PPPq4i")
+
+
+class Calls:
+    """The library's calls with their C signatures."""
+
+    def __init__(self):
+        L, P, I64, I = nv.lib(), ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+        F, DESC = ctypes.c_float, ctypes.c_char_p
+        for name, args in dict(
+                nvfp4_rms_norm=[P, I64, P, I64, P, F, P, I64, P, P, I64, I64, I64, I, P],
+                nvfp4_rope_apply=[DESC, P, I64, I64, P, I64, I64, I64, I64, I64, I, P],
+                nvfp4_kv_append=[DESC, DESC, P, I64, I64, P, I64, I64, I64, P, I64, I64, P, I64, I64, P, I64, I, P],
+                nvfp4_kv_read=[DESC, P, P, I64, I64, P, I64, I64, I64, I, P],
+                nvfp4_paged_attention=[DESC, P, I64, I64, P, I64, I64, P, I64, I64, F, I64, P, I64, I64, P, P, I64, I, P],
+        ).items():
+            f = ctypes.CFUNCTYPE(I, *args)((name, L))
+            setattr(self, name, f)
+
+
+@pytest.fixture(scope="module")
+def L():
+    return Calls()
 
 
 def last():
@@ -24,14 +50,14 @@ def last():
 def cache(**kw):
     a = dict(k=A, v=A, ks=0, vs=0, kst=(65536, 4096, 256), vst=(65536, 4096, 256), pages=10, page=16, heads=4, D=128, fmt=0)
     a.update(kw)
-    return at._KV_STRUCT.pack(a["k"], a["v"], a["ks"], a["vs"], *a["kst"], *a["vst"], a["pages"], a["page"], a["heads"],
+    return KV_STRUCT.pack(a["k"], a["v"], a["ks"], a["vs"], *a["kst"], *a["vst"], a["pages"], a["page"], a["heads"],
                               a["D"], a["fmt"])
 
 
 def rope(**kw):
     a = dict(inv=A, pos=A, pair=0, ld=8, axes=1, R=128, nb=0)
     a.update(kw)
-    return at._ROPE_STRUCT.pack(a["inv"], a["pos"], a["pair"], a["ld"], a["axes"], a["R"], a["nb"], 0)
+    return ROPE_STRUCT.pack(a["inv"], a["pos"], a["pair"], a["ld"], a["axes"], a["R"], a["nb"], 0)
 
 
 @pytest.mark.parametrize("kw,status,needle", [
@@ -43,10 +69,10 @@ def rope(**kw):
     (dict(x=A + 1), ALIGN, "misaligned"), (dict(y=A + 1), ALIGN, "misaligned"), (dict(scales=A + 2), ALIGN, "misaligned"),
     (dict(w=A + 1), ALIGN, "misaligned"), (dict(T=0), OK, ""), (dict(T=0, x=None, y=None, r=None), OK, ""),
 ])
-def test_norm_refusals(kw, status, needle):
+def test_norm_refusals(L, kw, status, needle):
     a = dict(x=A, ld_x=64, r=A, ld_r=64, w=A, eps=1e-6, y=A, ld_y=64, scales=None, h=None, ld_h=64, T=4, N=64)
     a.update(kw)
-    st = nv.lib().nvfp4_rms_norm(a["x"], a["ld_x"], a["r"], a["ld_r"], a["w"], a["eps"], a["y"], a["ld_y"], a["scales"],
+    st = L.nvfp4_rms_norm(a["x"], a["ld_x"], a["r"], a["ld_r"], a["w"], a["eps"], a["y"], a["ld_y"], a["scales"],
                                  a["h"], a["ld_h"], a["T"], a["N"], 0, None)
     assert st == status and needle in last()
 
@@ -63,10 +89,10 @@ def test_norm_refusals(kw, status, needle):
     (dict(rope=rope(ld=3)), INVALID, "ld_pos"), (dict(rope=rope(inv=A + 2)), ALIGN, "4-byte"),
     (dict(T=0), OK, ""), (dict(H=0), OK, ""),
 ])
-def test_rope_refusals(kw, status, needle):
+def test_rope_refusals(L, kw, status, needle):
     a = dict(rope=rope(), x=A, x_t=1024, x_h=128, o=A, o_t=1024, o_h=128, T=4, H=8, D=128)
     a.update(kw)
-    st = nv.lib().nvfp4_rope_apply(a["rope"], a["x"], a["x_t"], a["x_h"], a["o"], a["o_t"], a["o_h"], a["T"], a["H"], a["D"],
+    st = L.nvfp4_rope_apply(a["rope"], a["x"], a["x_t"], a["x_h"], a["o"], a["o_t"], a["o_h"], a["T"], a["H"], a["D"],
                                    0, None)
     assert st == status and needle in last()
 
@@ -84,8 +110,7 @@ BAD_CACHES = [
 
 
 @pytest.mark.parametrize("desc,status,needle", BAD_CACHES)
-def test_cache_refusals(desc, status, needle):
-    L = nv.lib()
+def test_cache_refusals(L, desc, status, needle):
     assert L.nvfp4_kv_append(desc, None, None, 0, 0, None, 0, 0, 0, A, 512, 128, A, 512, 128, A, 4, 0, None) == status
     assert needle in last()
     assert L.nvfp4_kv_read(desc, A, A, 512, 128, A, 512, 128, 4, 0, None) == status and needle in last()
@@ -101,10 +126,10 @@ def test_cache_refusals(desc, status, needle):
     (dict(desc=cache(fmt=2), rope=rope(R=48)), INVALID, "multiple of 32"), (dict(T=0), OK, ""),
     (dict(T=0, rope=rope(pos=0), Hq=4, slots=None), OK, ""),
 ])
-def test_append_refusals(kw, status, needle):
+def test_append_refusals(L, kw, status, needle):
     a = dict(desc=cache(), rope=None, q=A, qo=A, Hq=0, k=A, k_t=512, v=A, slots=A, T=4)
     a.update(kw)
-    st = nv.lib().nvfp4_kv_append(a["desc"], a["rope"], a["q"], 1024, 128, a["qo"], 1024, 128, a["Hq"], a["k"], a["k_t"], 128,
+    st = L.nvfp4_kv_append(a["desc"], a["rope"], a["q"], 1024, 128, a["qo"], 1024, 128, a["Hq"], a["k"], a["k_t"], 128,
                                   a["v"], 512, 128, a["slots"], a["T"], 0, None)
     assert st == status and needle in last()
 
@@ -119,10 +144,10 @@ def test_append_refusals(kw, status, needle):
     (dict(ws=None), SMALL, "workspace"), (dict(ws=A + 16), ALIGN, "256-byte"), (dict(B=0), OK, ""),
     (dict(B=0, q=None, table=None, ws=None), OK, ""),
 ])
-def test_attention_refusals(kw, status, needle):
+def test_attention_refusals(L, kw, status, needle):
     a = dict(q=A, table=A, ld=100, pages=100, lengths=A, B=2, Hq=8, scale=0.1, window=0, out=A, lse=A, ws=A, wsb=1 << 30)
     a.update(kw)
-    st = nv.lib().nvfp4_paged_attention(cache(), a["q"], 1024, 128, a["table"], a["ld"], a["pages"], a["lengths"], a["B"],
+    st = L.nvfp4_paged_attention(cache(), a["q"], 1024, 128, a["table"], a["ld"], a["pages"], a["lengths"], a["B"],
                                         a["Hq"], a["scale"], a["window"], a["out"], 1024, 128, a["lse"], a["ws"], a["wsb"], 0,
                                         None)
     assert st == status and needle in last()
@@ -141,45 +166,31 @@ def test_workspace_sizes():
 # -------------------------------------------------------------- the binding --
 
 def test_binding_checks():
-    """Tensors that are not on the GPU, of other types or shapes raise ValueError before the library is called."""
+    """Tensors that are not on the GPU or of other types raise ValueError before the library is called."""
     x = torch.ones((2, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="on the GPU"):
         nv.rms_norm(x, x[0])
     with pytest.raises(ValueError, match="bf16 or fp16"):
         nv.rms_norm(x.float(), x[0])
+    with pytest.raises(ValueError, match="bf16 or fp16"):
+        nv.rms_norm_fp8("x", x[0])
     with pytest.raises(ValueError, match="on the GPU"):
         nv.rope(torch.ones((2, 2, 64), dtype=torch.float16), None, None)
     with pytest.raises(ValueError, match="on the GPU"):
         nv.kv_read(x, x, x)
+    with pytest.raises(ValueError, match="torch tensor"):
+        nv.kv_read(None, x, x)
+    with pytest.raises(ValueError, match="on the GPU"):
+        nv.kv_write(*[x.view(2, 1, 64)] * 2, x, x, x)
+    with pytest.raises(ValueError, match="bf16 or fp16"):
+        nv.rope_kv_write(None, x, x, x, x, x, x, x)
+    with pytest.raises(ValueError, match="bf16 or fp16"):
+        nv.kv_read(x, x, x, torch.float32)
+    with pytest.raises(ValueError, match="on the GPU"):
+        nv.paged_attention(x.view(2, 1, 64), x, x, x, x)
     with pytest.raises(ValueError, match="cache dtype"):
         nv.kv_cache(2, 2, 16, 64, torch.float32, "cpu")
-    dev = torch.device("cpu")
-    bf = nv.kv_cache(3, 2, 16, 64, torch.bfloat16, "cpu")
-    f8 = nv.kv_cache(3, 2, 16, 64, torch.float8_e4m3fn, "cpu")
-    f4 = nv.kv_cache(3, 2, 16, 64, torch.uint8, "cpu")
-    assert f4[0].shape == (3, 2, 16, 36)
-    one = torch.ones(2)
-    desc, heads, D, pages, page = at._pack_cache(*f4, one, None, torch.float16, dev)
-    assert (heads, D, pages, page) == (2, 64, 3, 16) and len(desc) == at._KV_STRUCT.size
-    bad = [
-        ((bf[0], f8[0], None, None), "one dtype"), ((bf[0], bf[1][:2], None, None), "one shape"),
-        ((*bf, one, None), "takes no k_scale"), ((*f8, None, torch.ones(3)), "v_scale"),
-        ((*f8, one.half(), None), "k_scale"), ((f8[0].transpose(2, 3),) * 2 + (None, None), "contiguous rows"),
-        ((f4[0].transpose(1, 2),) * 2 + (None, None), "contiguous blocks"),
-        ((f4[0][..., :35],) * 2 + (None, None), "contiguous blocks"), ((bf[0].float(),) * 2 + (None, None), "must be a bf16"),
-        ((torch.zeros((2, 2, 16, 45), dtype=torch.uint8),) * 2 + (None, None), "multiple of 32"),
-    ]
-    for args, needle in bad:
-        with pytest.raises(ValueError, match=needle):
-            at._pack_cache(*args, torch.bfloat16, dev)
-    with pytest.raises(ValueError, match="activations"):
-        at._pack_cache(*bf, None, None, torch.float16, dev)
-    inv, pos = torch.ones(32), torch.zeros((3, 5), dtype=torch.int32)
-    for args, needle in [((pos, inv, None, False, 5, dev), "need pair_axis"), ((pos, inv, None, False, 4, dev), "positions"),
-                         ((pos.long(), inv, inv.int(), False, 5, dev), "positions"), ((pos[0], inv.double(), None, False, 5, dev), "inv_freq"),
-                         ((pos, inv, torch.zeros(31, dtype=torch.int32), False, 5, dev), "pair_axis")]:
-        with pytest.raises(ValueError, match=needle):
-            at._pack_rope(*args)
+    assert nv.kv_cache(3, 2, 16, 64, torch.uint8, "cpu")[0].shape == (3, 2, 16, 36)
 
 
 def test_pair_axis_sections():
@@ -242,5 +253,5 @@ def test_rope_forms_agree():
 
 def test_descriptor_layouts():
     """The packed descriptors have the C structs' sizes (pointers and 64-bit fields first, no padding)."""
-    assert at._KV_STRUCT.size == 4 * ctypes.sizeof(ctypes.c_void_p) + 7 * 8 + 4 * 4
-    assert at._ROPE_STRUCT.size == 3 * ctypes.sizeof(ctypes.c_void_p) + 8 + 4 * 4
+    assert KV_STRUCT.size == 4 * ctypes.sizeof(ctypes.c_void_p) + 7 * 8 + 4 * 4
+    assert ROPE_STRUCT.size == 3 * ctypes.sizeof(ctypes.c_void_p) + 8 + 4 * 4

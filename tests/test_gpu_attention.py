@@ -53,8 +53,8 @@ def test_norm(T, N, dt, res, pad, fp8):
     xd, rd = strided(x, pad), strided(r, pad)
     call = nv.rms_norm_fp8 if fp8 else nv.rms_norm
     got = call(xd, w.to(DEV), eps, residual=rd if res else None)
-    got = got if isinstance(got, tuple) else (got,)
     h = x
+    assert (got[-1] is None) == (not res)
     if res:
         h = (x.float() + r.float()).to(dt)
         assert torch.equal(got[-1].cpu().view(torch.int16), h.view(torch.int16))
@@ -87,7 +87,7 @@ def test_norm_in_place_and_edge_rows(N):
         fresh = call(x.to(DEV), w, 1e-6, residual=r.to(DEV))
         rd = r.to(DEV)
         got = call(x.to(DEV), w, 1e-6, residual=rd, residual_out=rd)
-        assert got[-1] is rd
+        assert got[-1].data_ptr() == rd.data_ptr()
         for a, b in zip(fresh, got):
             assert torch.equal(a.float().nan_to_num(99), b.float().nan_to_num(99))
         y = got[0].float()
@@ -549,12 +549,73 @@ def test_empty_calls():
     assert nv.rope(z, none, inv).shape == (0, 2, 64)
     assert nv.rope_kv_write(z, z, z, none, inv, kc, vc, none).shape == (0, 2, 64)
     assert nv.kv_read(kc, vc, none)[0].shape == (0, 2, 64)
-    assert nv.rms_norm(torch.empty((0, 64), dtype=BF, device=DEV), torch.ones(64, dtype=BF, device=DEV)).shape == (0, 64)
+    assert nv.rms_norm(torch.empty((0, 64), dtype=BF, device=DEV), torch.ones(64, dtype=BF, device=DEV))[0].shape == (0, 64)
     assert nv.paged_attention(z, kc, vc, torch.empty((0, 1), dtype=torch.int32, device=DEV), none).shape == (0, 2, 64)
     q = torch.ones((2, 2, 64), dtype=BF, device=DEV)
     out, lse = nv.paged_attention(q, kc, vc, torch.empty((2, 0), dtype=torch.int32, device=DEV),
                                   torch.tensor([5, 0], dtype=torch.int32, device=DEV), return_lse=True)
     assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
+
+
+def test_binding_refusals():
+    """Wrong shapes, types, devices and caches raise before anything runs; a refusal by the library is an Nvfp4Error."""
+    x, w = torch.ones((2, 64), dtype=BF, device=DEV), torch.ones(64, dtype=BF, device=DEV)
+    bad = [
+        (lambda: nv.rms_norm(x, w[:32]), "weight"), (lambda: nv.rms_norm(x, w.half()), "weight"),
+        (lambda: nv.rms_norm(x, w.cpu()), "weight is on cpu"), (lambda: nv.rms_norm(x.t(), w), "unit stride"),
+        (lambda: nv.rms_norm(x, w, residual=x[:1]), "residual"), (lambda: nv.rms_norm(x[0], w), "2 dims"),
+        (lambda: nv.rms_norm(x, w, residual_out=x), "needs a residual"), (lambda: nv.rms_norm(x, w, out=x.half()), "out"),
+        (lambda: nv.rms_norm_fp8(x, w, scales=w), "scales"),
+    ]
+    h = torch.ones((5, 4, 64), dtype=BF, device=DEV)
+    inv, pos = torch.ones(32, device=DEV), torch.zeros((3, 5), dtype=torch.int32, device=DEV)
+    axis = torch.zeros(32, dtype=torch.int32, device=DEV)
+    bad += [
+        (lambda: nv.rope(h, pos, inv), "need pair_axis"), (lambda: nv.rope(h, pos[:, :4], inv, axis), "positions"),
+        (lambda: nv.rope(h, pos.long(), inv, axis), "positions"), (lambda: nv.rope(h, pos[0], inv.double()), "inv_freq"),
+        (lambda: nv.rope(h, pos, inv, axis[:31]), "pair_axis"), (lambda: nv.rope(h[0], pos, inv, axis), "3 dims"),
+        (lambda: nv.rope(h, pos[0], inv[None]), "1-d"),
+    ]
+    one = torch.ones(2, device=DEV)
+    bf, f8, f4 = (nv.kv_cache(3, 2, 16, 64, d, DEV) for d in (BF, torch.float8_e4m3fn, torch.uint8))
+    k, slots = h[:, :2], torch.zeros(5, dtype=torch.int32, device=DEV)
+    odd = torch.zeros((2, 2, 16, 45), dtype=torch.uint8, device=DEV)
+
+    def write(kc, vc, ks=None, vs=None, k=k, v=k, slots=slots):
+        return lambda: nv.kv_write(k, v, kc, vc, slots, k_scale=ks, v_scale=vs)
+
+    bad += [
+        (write(bf[0], f8[0]), "one dtype"), (write(bf[0], bf[1][:2]), "one shape"), (write(*bf, one), "takes no k_scale"),
+        (write(*f8, None, one[:1]), "v_scale"), (write(*f8, one.half()), "k_scale"),
+        (write(*(f8[0].transpose(2, 3),) * 2), "contiguous rows"), (write(*(f4[0].transpose(1, 2),) * 2), "contiguous blocks"),
+        (write(*(f4[0][..., :35],) * 2), "contiguous blocks"), (write(*(bf[0].float(),) * 2), "must be a bf16"),
+        (write(odd, odd), "multiple of 32"), (write(*bf, k=k.half(), v=k.half()), "activations"), (write(*bf, v=h), "v must be"),
+        (write(*bf, slots=slots.long()), "slots"), (write(bf[0].cpu(), bf[1]), "caches are on"),
+        (lambda: nv.kv_read(*bf, slots[None]), "1-d"), (lambda: nv.kv_read(*bf, slots, HF), "activations"),
+        (lambda: nv.kv_read(*bf, slots, out=(h, h)), "out"),
+    ]
+    q, table, n = h, torch.zeros((5, 2), dtype=torch.int32, device=DEV), slots
+    bad += [
+        (lambda: nv.paged_attention(q[..., :32].contiguous(), *bf, table, n), "columns a head"),
+        (lambda: nv.paged_attention(q[:, :3], *bf, table, n), "multiple"),
+        (lambda: nv.paged_attention(q, *bf, table[:4], n), "page_table"), (lambda: nv.paged_attention(q, *bf, table.long(), n), "page_table"),
+        (lambda: nv.paged_attention(q, *bf, table, n[:4]), "lengths"),
+        (lambda: nv.paged_attention(q, *bf, table, n, workspace_buf=torch.zeros(8)), "workspace_buf"),
+    ]
+    for call, needle in bad:
+        with pytest.raises(ValueError, match=needle):
+            call()
+    with pytest.raises(nv.Nvfp4Error, match="window"):
+        nv.paged_attention(q, *bf, table, n, window=-1)
+    wide = torch.zeros((5, 20), dtype=torch.int32, device=DEV)
+    with pytest.raises(nv.Nvfp4Error, match="BUFFER_TOO_SMALL.*workspace"):
+        nv.paged_attention(q, *bf, wide, n, workspace_buf=torch.zeros(8, device=DEV))
+    with pytest.raises(nv.Nvfp4Error, match="rotary"):
+        nv.rope(h, pos[0], inv[:4])
+    with pytest.raises(nv.Nvfp4Error, match="eps"):
+        nv.rms_norm(x, w, -1.0)
+    with pytest.raises(TypeError):
+        nv.rms_norm(x, w, "eps")
 
 
 def test_a_captured_step_replays():

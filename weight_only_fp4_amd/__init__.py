@@ -120,21 +120,9 @@ def lib() -> ctypes.CDLL:
         L.nvfp4_w4a16_grouped_gemm_variant.argtypes = [P, I64, I64, P, P, P, P, P, I, I, P, I64, I64, I64, I64, I64,
                                                        I, I, I, P]
         L.nvfp4_w4a16_grouped_gemm_variant.restype = I
-        F, DESC = ctypes.c_float, ctypes.c_char_p   # DESC: a packed descriptor (nvfp4_rope, nvfp4_kv_cache)
-        L.nvfp4_rms_norm.argtypes = [P, I64, P, I64, P, F, P, I64, P, P, I64, I64, I64, I, P]
-        L.nvfp4_rms_norm.restype = I
-        L.nvfp4_rope_apply.argtypes = [DESC, P, I64, I64, P, I64, I64, I64, I64, I64, I, P]
-        L.nvfp4_rope_apply.restype = I
-        L.nvfp4_kv_append.argtypes = [DESC, DESC, P, I64, I64, P, I64, I64, I64, P, I64, I64, P, I64, I64, P, I64, I,
-                                      P]
-        L.nvfp4_kv_append.restype = I
-        L.nvfp4_kv_read.argtypes = [DESC, P, P, I64, I64, P, I64, I64, I64, I, P]
-        L.nvfp4_kv_read.restype = I
+        # (the attention half's calls are bound in csrc/binding.cpp)
         L.nvfp4_paged_attention_workspace_bytes.argtypes = [I64, I64, I64, I64, I64]
         L.nvfp4_paged_attention_workspace_bytes.restype = I64
-        L.nvfp4_paged_attention.argtypes = [DESC, P, I64, I64, P, I64, I64, P, I64, I64, F, I64, P, I64, I64, P, P,
-                                            I64, I, P]
-        L.nvfp4_paged_attention.restype = I
         _lib = L
     return _lib
 

@@ -1,4 +1,4 @@
-"""Build the HIP library ``libnvfp4_w4a16.so`` in-tree for gfx950.
+"""Build the HIP library ``libnvfp4_w4a16.so`` in-tree for gfx950, and the Python binding of its attention half.
 
     python -m weight_only_fp4_amd.build
 """
@@ -19,6 +19,7 @@ else:   # run as a script
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libnvfp4_w4a16.so")
+BINDING = os.path.join(HERE, "_attention.so")   # Python binding of the attention half, linked against LIB
 ARCH = "gfx950"
 
 COMMON = [
@@ -58,7 +59,7 @@ def _run(cmd):
     res = subprocess.run(cmd, capture_output=True, text=True)
     msgs = "\n".join(l for l in (res.stdout + res.stderr).splitlines() if NOISE not in l and l.strip())
     if res.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + " ".join(cmd) + "\n" + msgs)
+        raise RuntimeError(os.path.basename(cmd[0]) + " failed:\n" + " ".join(cmd) + "\n" + msgs)
     return msgs
 
 
@@ -77,8 +78,29 @@ def _check_asm(cmd, path):
     return ""
 
 
+def _build_binding(rocm: str):
+    """Compile csrc/binding.cpp (host code only) against the installed torch and the library beside it."""
+    import sysconfig
+
+    import torch
+
+    t = os.path.dirname(os.path.abspath(torch.__file__))
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", os.path.join(t, "include"),
+           "-isystem", os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(rocm, "include"), "-I" + sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L" + os.path.join(t, "lib"), "-lc10", "-lc10_hip",
+           "-ltorch_cpu", "-ltorch_python", "-L" + HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+    msgs = _run(cmd)
+    os.replace(tmp, BINDING)
+    return cmd, msgs
+
+
 def build(verbose: bool = False) -> str:
-    hipcc = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "bin", "hipcc")
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    hipcc = os.path.join(rocm, "bin", "hipcc")
     with tempfile.TemporaryDirectory(prefix="nvfp4_build_") as tmpd:
         jobs, checks = [], []
         for src, extra, tag in SOURCES:
@@ -105,6 +127,11 @@ def build(verbose: bool = False) -> str:
             if msgs:
                 print(msgs, flush=True)
     os.replace(tmp, LIB)
+    cmd, msgs = _build_binding(rocm)
+    if verbose:
+        print(" ".join(cmd), flush=True)
+        if msgs:
+            print(msgs, flush=True)
     return LIB
 
 
