@@ -19,24 +19,23 @@ struct AttnShape {
 // A split call's counters, one a workgroup, at the workspace's start: partial
 // results of calls of other sizes never reach them.
 constexpr int64_t kAttnCounterBytes = kAttnMaxWorkgroups * 4;
-// At most this many workgroups per pair on average, which bounds what the last
-// of them has to join.
-constexpr int64_t kAttnPairSplits = 64;
-
-inline AttnShape attn_shape(int64_t B, int64_t Hk, int64_t G, int64_t D, int64_t max_tokens, int64_t target) {
+// Two workgroups per compute unit (the kernels take up to 256 registers a
+// lane, so eight waves fit a unit): one works while the other ends a segment.
+// Only places the lengths can give count (kernels_attn.h).
+inline AttnShape attn_shape(int64_t B, int64_t Hk, int64_t G, int64_t D, int64_t max_tokens) {
     AttnShape s;
     s.pairs = B * Hk * ((G + kAttnHeads - 1) / kAttnHeads);
     s.part_floats = (G < kAttnHeads ? G : kAttnHeads) * (D + 2);
-    // places of the row of units (kernels_attn.h), as many as the lengths can give
     const int64_t units = (max_tokens + kAttnTile + kAttnUnit - 1) / kAttnUnit;
-    s.split = B <= kAttnScan && max_tokens > kAttnUnit && s.pairs * (units + 1) < ((int64_t)1 << 31);
+    const int64_t places = s.pairs * (units + 1);
+    s.split = B <= kAttnScan && places >= 8 && places < ((int64_t)1 << 31);
     s.workgroups = s.pairs;
     if (s.split) {
-        s.workgroups = target;
-        if (s.workgroups > s.pairs * kAttnPairSplits) s.workgroups = s.pairs * kAttnPairSplits;
-        if (s.workgroups > s.pairs * units) s.workgroups = s.pairs * units;
+        int64_t each = units / 4 + 1;
+        if (each > kAttnPairSplits) each = kAttnPairSplits;
+        s.workgroups = s.pairs * each < kAttnMaxWorkgroups ? s.pairs * each : kAttnMaxWorkgroups;
     }
-    s.total = s.split && s.pairs > 0 ? kAttnCounterBytes + (int64_t)kAttnMaxWorkgroups * 2 * s.part_floats * 4 : 0;
+    s.total = s.split && units > 1 ? kAttnCounterBytes + (int64_t)kAttnMaxWorkgroups * 2 * s.part_floats * 4 : 0;
     return s;
 }
 

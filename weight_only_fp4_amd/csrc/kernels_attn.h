@@ -33,13 +33,15 @@ struct AttnArgs {
     int* counters;               // [workgroups], zero between calls
 };
 
-constexpr int kAttnWaves = 8;
+constexpr int kAttnWaves = 4;
 constexpr int kAttnThreads = kAttnWaves * 64;
 constexpr int kAttnTile = 32;                               // tokens a wave takes at a time
 constexpr int kAttnUnit = kAttnWaves * kAttnTile;           // tokens a workgroup takes at a time
 constexpr int kAttnHeads = 16;                              // query heads of one workgroup
 constexpr int kAttnScan = 2048;                             // sequences whose unit counts are kept in LDS
 constexpr int kAttnMaxWorkgroups = 512;                     // of a split call
+constexpr int kAttnPairSplits = 64;                         // at most this many workgroups per pair on average: the
+                                                            // last of them joins what they leave
 constexpr int kAttnOutCols = 64;                            // columns of the accumulators that go through LDS at a time
 
 // Read-only memory at a uniform address (scalar loads), and rows of the cache.
@@ -85,6 +87,20 @@ __device__ __forceinline__ float attn_head_max(float v) {
     return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
+// Maximum / sum over the wave in registers: lanes 32 and 16 apart change places,
+// then the rows of 16 lanes rotate by 8, 4, 2 and 1.
+template <typename Op>
+__device__ __forceinline__ float attn_wave_reduce(float v, Op op) {
+    auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    v = op(v, __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x128, 0xF, 0xF, true)));
+    v = op(v, __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x124, 0xF, 0xF, true)));
+    v = op(v, __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x122, 0xF, 0xF, true)));
+    return op(v, __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x121, 0xF, 0xF, true)));
+}
+
 // Streaming loads: the cache's rows are read once.
 template <int BYTES>
 __device__ __forceinline__ void attn_load(AttnRow p, uint32_t* d) {
@@ -108,13 +124,16 @@ __device__ __forceinline__ void attn_load(AttnRow p, uint32_t* d) {
     }
 }
 
-// The work.  A sequence's tokens are cut into units of 256 (kAttnUnit); its
+// The work.  A sequence's tokens are cut into units of 128 (kAttnUnit); its
 // key-value heads (times tiles of 16 query heads) all have that many.  The
 // units of all (sequence, head) pairs stand in one row, sequence by sequence,
 // each pair with one more place in front for what a pair costs besides its
-// tokens, and every workgroup takes an equal stretch of the row, so every
-// compute unit gets the same work whatever the lengths are.  A stretch is a
-// few segments, each a run of units of one pair; a segment that is not the
+// tokens, and workgroup j of N takes the places from floor(j P / N) to
+// floor((j + 1) P / N) of all P, so every compute unit gets the same work
+// whatever the lengths are.  N is a multiple of the pairs while that leaves
+// four places a workgroup (pairs of equal lengths are then split at equal
+// places and short ones not at all), and at most the grid.  A stretch is a few
+// segments, each a run of units of one pair; a segment that is not the
 // whole pair leaves a partial result, and the workgroup that arrives last at
 // a pair adds the partial results in their order (so the result does not
 // depend on timing).
@@ -193,7 +212,11 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
     };
 
     // ---- this workgroup's stretch of places [p_begin, p_end)
-    int p_begin, p_end, stretch = 0, b = 0;
+    int p_begin, p_end, groups = 1, b = 0;
+    unsigned places = 1;
+    // floor(x / y) of a 41-bit and a 31-bit number, exact in fp64: the quotient is
+    // further from the next integer than it is rounded by
+    auto quotient = [](int64_t x, unsigned y) { return (int)((double)x / (double)y); };
     if (!a.split) {
         b = (int)(blockIdx.x / (unsigned)HT);
         p_begin = 0;
@@ -226,11 +249,13 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
             if (lane == 0) s_pre[0] = 0;
         }
         __syncthreads();
-        const unsigned places = (unsigned)__builtin_amdgcn_readfirstlane(s_pre[a.B]) * (unsigned)HT;   // below 2^31
-        stretch = (int)((places + gridDim.x - 1) / gridDim.x);
-        if (blockIdx.x * (int64_t)stretch >= places) return;
-        p_begin = (int)blockIdx.x * stretch;
-        p_end = places - (unsigned)p_begin < (unsigned)stretch ? (int)places : p_begin + stretch;
+        places = (unsigned)__builtin_amdgcn_readfirstlane(s_pre[a.B]) * (unsigned)HT;   // below 2^31
+        const unsigned pairs = (unsigned)(a.B * HT), each = places / (4u * pairs);
+        groups = (int)(pairs * (each < 1 ? 1 : (each > kAttnPairSplits ? kAttnPairSplits : each)));
+        groups = groups < (int)gridDim.x ? groups : (int)gridDim.x;
+        if ((int)blockIdx.x >= groups) return;
+        p_begin = quotient((int64_t)blockIdx.x * places, groups);
+        p_end = quotient((int64_t)(blockIdx.x + 1) * places, groups);
         int lo = 0, hi = a.B;   // the sequence of the first place: the last b with HT * s_pre[b] <= p_begin
         const int at = p_begin / HT;
         while (hi - lo > 1) {
@@ -662,31 +687,69 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
         // The workgroups of the pair: the one holding its first unit (of which
         // this can be the only pair that goes on past its stretch: the counter
         // is that workgroup's) to the one holding its last.
-        const int j0 = (pair_begin + 1) / stretch, j1 = (pair_begin + units) / stretch;
+        // Workgroup j holds place p if it is the last with floor(j P / N) <= p.
+        const int j0 = quotient((int64_t)groups * (pair_begin + 2) - 1, places);
+        const int j1 = quotient((int64_t)groups * (pair_begin + units + 1) - 1, places);
         const int parts = j1 - j0 + 1;
         if (!split_arrive(z->counters, j0, parts, &s_flag)) continue;
         // ---- the workgroup that arrived last joins all of them, in their
-        // order.  Each thread's first loads are under way while the factor of
-        // every (partial result, head), exp2(its maximum - the largest) over
-        // the sum of weights, is worked out into LDS, a wave per head and a
-        // lane per partial result.
-        const float* parts0 = z->partials + (int64_t)(j0 * 2 + (j0 * stretch < pair_begin ? 1 : 0)) * part_floats;   // of j0
-        const float* parts1 = z->partials + (int64_t)j0 * 2 * part_floats;   // of j0 + x, x > 0: 2 x further
-        auto load2 = [&](int x, int at) {
-            const float* from = (x == 0 ? parts0 : parts1 + (int64_t)x * 2 * part_floats) + at;
+        // order: the sum of (factor x partial sums), the factor of a (partial
+        // result, head) being exp2(its maximum - the largest) over the sum of
+        // weights.
+        // workgroup j0's is its first partial result or its second, the others' are their first
+        const int second = quotient((int64_t)j0 * places, groups) < pair_begin ? part_floats : 0;
+        const float* parts0 = z->partials + (int64_t)j0 * 2 * part_floats;
+        auto load2 = [&](const float* from) {
             return __hip_atomic_load(reinterpret_cast<const uint64_t*>(from), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         };
-        float* s_f = s_o;   // [parts][nh]
         const int half = D / 2;
         constexpr int kJoinLoads = 16;
         uint64_t v[kJoinLoads];
-        int i = threadIdx.x;
-        auto fetch = [&](int i, int x0) {
-            const int at = i < nh * half ? (i / half) * D + (i % half) * 2 : 0;
+        auto fetch = [&](const float* from, int x0) {   // partial results x0 .. (the last one again past the end)
+            from += (int64_t)x0 * 2 * part_floats + (x0 == 0 ? second : 0);
 #pragma unroll
-            for (int x = 0; x < kJoinLoads; ++x) v[x] = load2(x0 + x < parts ? x0 + x : 0, at);
+            for (int x = 0; x < kJoinLoads; ++x) {
+                v[x] = load2(from);
+                from += x0 + x + 1 < parts ? 2 * part_floats - (x0 + x == 0 ? second : 0) : 0;
+            }
         };
-        fetch(i, 0);
+        if (parts <= kJoinLoads) {
+            // few: each thread fetches its head's (maximum, sum) pairs with its
+            // columns and works the factors out itself, one round trip in all
+            for (int i = threadIdx.x; i < nh * half; i += kAttnThreads) {
+                const int h = i / half, d = (i - h * half) * 2;
+                uint64_t ml[kJoinLoads];
+                fetch(parts0 + hp * D + 2 * h, 0);
+#pragma unroll
+                for (int x = 0; x < kJoinLoads; ++x) ml[x] = v[x];
+                fetch(parts0 + h * D + d, 0);
+                float mm = __uint_as_float((uint32_t)ml[0]);
+#pragma unroll
+                for (int x = 1; x < kJoinLoads; ++x) mm = fmaxf(mm, __uint_as_float((uint32_t)ml[x]));
+                float ll = 0.f, o0 = 0.f, o1 = 0.f;
+#pragma unroll
+                for (int x = 0; x < kJoinLoads; ++x) {
+                    const float mx = __uint_as_float((uint32_t)ml[x]);
+                    const float f = x >= parts || mx == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mx - mm);
+                    if (x < parts) {
+                        ll = __builtin_fmaf(f, __uint_as_float((uint32_t)(ml[x] >> 32)), ll);
+                        o0 = __builtin_fmaf(f, __uint_as_float((uint32_t)v[x]), o0);
+                        o1 = __builtin_fmaf(f, __uint_as_float((uint32_t)(v[x] >> 32)), o1);
+                    }
+                }
+                const float inv = ll == 0.f ? 0.f : vscale / ll;
+                store_out(h, d, o0 * inv, o1 * inv);
+                if (d == 0) store_lse(h, mm, ll);
+            }
+            __syncthreads();
+            continue;
+        }
+        // many: the factors go through LDS, a wave per head and a lane per
+        // partial result, while each thread's first loads are under way
+        float* s_f = s_o;   // [parts][nh]
+        int i = threadIdx.x;
+        auto columns = [&](int i) { return parts0 + (i < nh * half ? (i / half) * D + (i % half) * 2 : 0); };
+        fetch(columns(i), 0);
         for (int h = w; h < nh; h += kAttnWaves) {
             constexpr int LANE_PARTS = kAttnMaxWorkgroups / 64;
             float mx[LANE_PARTS], lx[LANE_PARTS];
@@ -695,24 +758,23 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
             for (int y = 0; y < LANE_PARTS; ++y) {
                 mx[y] = -INFINITY;
                 lx[y] = 0.f;
-                if (lane + 64 * y < parts) {
-                    const uint64_t ml = load2(lane + 64 * y, hp * D + 2 * h);
+                const int x = lane + 64 * y;
+                if (x < parts) {
+                    const uint64_t ml = load2(parts0 + (int64_t)x * 2 * part_floats + (x == 0 ? second : 0) + hp * D + 2 * h);
                     mx[y] = __uint_as_float((uint32_t)ml);
                     lx[y] = __uint_as_float((uint32_t)(ml >> 32));
                 }
             }
 #pragma unroll
             for (int y = 0; y < LANE_PARTS; ++y) mm = fmaxf(mm, mx[y]);
-#pragma unroll
-            for (int d = 32; d >= 1; d >>= 1) mm = fmaxf(mm, __shfl_xor(mm, d));
+            mm = attn_wave_reduce(mm, [](float p, float q) { return fmaxf(p, q); });
             float ll = 0.f;
 #pragma unroll
             for (int y = 0; y < LANE_PARTS; ++y) {
                 mx[y] = mx[y] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mx[y] - mm);
                 ll += mx[y] * lx[y];
             }
-#pragma unroll
-            for (int d = 32; d >= 1; d >>= 1) ll += __shfl_xor(ll, d);
+            ll = attn_wave_reduce(ll, [](float p, float q) { return p + q; });
             const float inv = ll == 0.f ? 0.f : vscale / ll;
 #pragma unroll
             for (int y = 0; y < LANE_PARTS; ++y)
@@ -733,12 +795,12 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
                 }
                 x0 += kJoinLoads;
                 if (x0 >= parts) break;
-                fetch(i, x0);
+                fetch(columns(i), x0);
             }
             if (i < nh * half) store_out(h, (i - h * half) * 2, o0, o1);
             i += kAttnThreads;
             if (i - (int)threadIdx.x >= nh * half) break;
-            fetch(i, 0);
+            fetch(columns(i), 0);
         }
         __syncthreads();
     }

@@ -35,7 +35,6 @@ void launch_norm(const NormArgs& a, bool vec, hipStream_t st) {
     else hipLaunchKernelGGL((k_rms_norm<F16, F8, 4>), grid, dim3(threads), 0, st, a);
 }
 
-constexpr int64_t kAttnWorkgroups = 256;   // of a split call: one per compute unit
 constexpr int64_t kNormVecMax = 1024 * 8 * 4;
 
 // ------------------------------------------------------------ cache checks --
@@ -334,7 +333,7 @@ extern "C" {
 
 int64_t nvfp4_paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t heads, int64_t D, int64_t max_tokens) {
     if (check_attn_sizes("nvfp4_paged_attention_workspace_bytes", B, Hq, heads, D, max_tokens) != NVFP4_OK) return -1;
-    return attn_shape(B, heads, Hq / heads, D, max_tokens, kAttnMaxWorkgroups).total;
+    return attn_shape(B, heads, Hq / heads, D, max_tokens).total;
 }
 
 nvfp4_status nvfp4_paged_attention(const nvfp4_kv_cache* cache, const void* q, int64_t q_b, int64_t q_h,
@@ -361,7 +360,7 @@ nvfp4_status nvfp4_paged_attention(const nvfp4_kv_cache* cache, const void* q, i
     if (!aligned(page_table, 4) || !aligned(lengths, 4) || !aligned(lse, 4))
         return fail(NVFP4_ERR_ALIGNMENT, "%s: page_table, lengths and lse must be 4-byte aligned", fn);
     const int64_t G = Hq / c.shape.heads;
-    const AttnShape sh = attn_shape(B, c.shape.heads, G, c.shape.D, max_tokens, kAttnWorkgroups);
+    const AttnShape sh = attn_shape(B, c.shape.heads, G, c.shape.D, max_tokens);
     if (sh.total > 0) {
         if (!workspace || workspace_bytes < sh.total)
             return fail(NVFP4_ERR_BUFFER_TOO_SMALL, "%s: workspace of %lld bytes is below the %lld bytes this call needs", fn,
