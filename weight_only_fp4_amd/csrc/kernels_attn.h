@@ -468,11 +468,13 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
                     }
                 }
             }
-            // ---- weights of the lane's eight tokens
+            // ---- weights of the lane's eight tokens (scaled first: a fused s qk - m
+            // would not be 0 at the maximum of very large scores)
             float s[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) s[i] = sc[i >> 2][i & 3] * qk_log2;
             if (x.valid != 0xFFFFFFFFu) {
+                asm volatile("");   // a branch: as selects the masks cost every tile 50 operations
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const bool ok = (x.valid >> ((i >> 2) * 16 + g * 4 + (i & 3))) & 1u;
@@ -503,44 +505,44 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
             }
             const uint4 pf = make_uint4(pack_round2<F16>(p[0], p[1]), pack_round2<F16>(p[2], p[3]),
                                         pack_round2<F16>(p[4], p[5]), pack_round2<F16>(p[6], p[7]));
-            // ---- values: 16-bit words of (token pair, column)
-            constexpr int HW = VD / 2;   // dwords of a lane's row in 16 bits
-            uint32_t vh[8][HW];
+            // ---- values, transposed: a dword holds one column of a token pair
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if constexpr (KV == kKv16) {
+            for (int e0 = 0; e0 < VD; e0 += 8) {
+                constexpr int EN = VD < 8 ? VD : 8;
+                uint32_t vt[4][EN];   // [token pair][column e0 + ..]
 #pragma unroll
-                    for (int y = 0; y < HW; ++y) vh[i][y] = x.vraw[i][y];
-                } else if constexpr (KV == kKvE4m3) {
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (KV == kKvNvfp4) {
+                        // the pair's codes of a column side by side in a byte, then
+                        // both values and both scales at once
+                        const uint32_t ca = x.vraw[2 * i][e0 / 8], cb = x.vraw[2 * i + 1][e0 / 8];
+                        const uint32_t even = (ca & 0x0F0F0F0Fu) | ((cb << 4) & 0xF0F0F0F0u);
+                        const uint32_t odd = ((ca >> 4) & 0x0F0F0F0Fu) | (cb & 0xF0F0F0F0u);
+                        const f16x2v gs = __builtin_bit_cast(f16x2v, f16_of_e4m3<false>(x.vsc[2 * i] | (x.vsc[2 * i + 1] << 8)));
+                        const uint4 ve = f16_of_nvfp4(even, gs), vo = f16_of_nvfp4(odd, gs);
+                        const uint32_t d[8] = {ve.x, vo.x, ve.y, vo.y, ve.z, vo.z, ve.w, vo.w};
 #pragma unroll
-                    for (int y = 0; y < HW; ++y)
-                        vh[i][y] = (y & 1) ? f16_of_e4m3<true>(x.vraw[i][y >> 1]) : f16_of_e4m3<false>(x.vraw[i][y >> 1]);
-                } else {
-                    const f16x2v gs = f16_group_scale(x.vsc[i], false);
-                    if constexpr (VD == 4) {
-                        vh[i][0] = f16_times(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(x.vraw[i][0], 1.0f, 0)), gs);
-                        vh[i][1] = f16_times(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(x.vraw[i][0], 1.0f, 1)), gs);
+                        for (int e = 0; e < EN; ++e) vt[i][e] = d[e];
                     } else {
 #pragma unroll
-                        for (int y = 0; y < VW; ++y) {
-                            const uint4 d = f16_of_nvfp4(x.vraw[i][y], gs);
-                            vh[i][4 * y] = d.x;
-                            vh[i][4 * y + 1] = d.y;
-                            vh[i][4 * y + 2] = d.z;
-                            vh[i][4 * y + 3] = d.w;
+                        for (int y = 0; y < EN / 2; ++y) {
+                            uint32_t p0, p1;   // columns (2 y, 2 y + 1) of either token
+                            if constexpr (KV == kKv16) {
+                                p0 = x.vraw[2 * i][e0 / 2 + y];
+                                p1 = x.vraw[2 * i + 1][e0 / 2 + y];
+                            } else {
+                                const uint32_t w0 = x.vraw[2 * i][e0 / 4 + y / 2], w1 = x.vraw[2 * i + 1][e0 / 4 + y / 2];
+                                p0 = (y & 1) ? f16_of_e4m3<true>(w0) : f16_of_e4m3<false>(w0);
+                                p1 = (y & 1) ? f16_of_e4m3<true>(w1) : f16_of_e4m3<false>(w1);
+                            }
+                            vt[i][2 * y] = __builtin_amdgcn_perm(p1, p0, 0x05040100u);
+                            vt[i][2 * y + 1] = __builtin_amdgcn_perm(p1, p0, 0x07060302u);
                         }
                     }
                 }
-            }
 #pragma unroll
-            for (int e = 0; e < VD; ++e) {
-                const uint32_t sel = (e & 1) ? 0x07060302u : 0x05040100u;
-                const int y = e >> 1;
-                const uint4 vf = make_uint4(__builtin_amdgcn_perm(vh[1][y], vh[0][y], sel),
-                                            __builtin_amdgcn_perm(vh[3][y], vh[2][y], sel),
-                                            __builtin_amdgcn_perm(vh[5][y], vh[4][y], sel),
-                                            __builtin_amdgcn_perm(vh[7][y], vh[6][y], sel));
-                acc[e] = mma16<F16>(vf, pf, acc[e]);
+                for (int e = 0; e < EN; ++e)
+                    acc[e0 + e] = mma16<F16>(make_uint4(vt[0][e], vt[1][e], vt[2][e], vt[3][e]), pf, acc[e0 + e]);
             }
         };
 
