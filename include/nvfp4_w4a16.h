@@ -504,7 +504,7 @@ nvfp4_status nvfp4_moe_fc1_f16(const void* x, int64_t ld_x, int64_t T, const int
  *   overlap.  2-byte alignment of rows suffices (1-byte for 8-bit y, 4-byte
  *   for scales); rows and leading dimensions of 16 bytes (8 for 8-bit y) and N
  *   a multiple of 8 up to 32768 take the one-pass kernel.
- * T == 0 launches nothing.  Errors: T < 0 or T >= 2^31, N < 1 or N >= 2^31, a leading dimension < N, eps
+ * T == 0 launches nothing.  Errors: T < 0 or 2^32 threads or more (T >= 2^22, more for short rows), N < 1 or N >= 2^31, a leading dimension < N, eps
  * negative or not finite, h without residual, NULL x / weight / y -> INVALID_ARG; misaligned -> ALIGNMENT. */
 nvfp4_status nvfp4_rms_norm(const void* x, int64_t ld_x, const void* residual, int64_t ld_r, const void* weight,
                             float eps, void* y, int64_t ld_y, float* scales, void* h, int64_t ld_h, int64_t T,
@@ -570,7 +570,7 @@ typedef struct {
 
 /* Rotates x [T][H][D] (strides x_t, x_h) into out (strides o_t, o_h), which may
  * be x itself with the same strides.  D a multiple of 16 in [16, 1024], R <=
- * min(D, 256).  T == 0 or H == 0 launches nothing.  Errors: sizes, NULL
+ * min(D, 256).  T == 0 or H == 0 launches nothing.  Errors: sizes (T < 2^24), NULL
  * pointers -> INVALID_ARG; rows or strides not multiples of 16 bytes,
  * misaligned arrays -> ALIGNMENT. */
 nvfp4_status nvfp4_rope_apply(const nvfp4_rope* rope, const void* x, int64_t x_t, int64_t x_h, void* out, int64_t o_t,

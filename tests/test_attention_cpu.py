@@ -87,7 +87,7 @@ def test_norm_refusals(L, kw, status, needle):
     (dict(D=512, rope=rope(R=272)), INVALID, "rotary"), (dict(rope=rope(axes=2)), INVALID, "pair_axis"),
     (dict(rope=rope(axes=17, pair=A)), INVALID, "axes"), (dict(rope=rope(axes=0)), INVALID, "axes"),
     (dict(rope=rope(ld=3)), INVALID, "ld_pos"), (dict(rope=rope(inv=A + 2)), ALIGN, "4-byte"),
-    (dict(T=0), OK, ""), (dict(H=0), OK, ""),
+    (dict(T=0), OK, ""), (dict(H=0), OK, ""), (dict(T=1 << 24, rope=rope(ld=1 << 24)), INVALID, "too many"),
 ])
 def test_rope_refusals(L, kw, status, needle):
     a = dict(rope=rope(), x=A, x_t=1024, x_h=128, o=A, o_t=1024, o_h=128, T=4, H=8, D=128)
@@ -142,7 +142,7 @@ def test_append_refusals(L, kw, status, needle):
     (dict(out=None), INVALID, "out is NULL"), (dict(table=None), INVALID, "page_table"), (dict(lengths=None), INVALID, "lengths"),
     (dict(q=A + 2), ALIGN, "q rows"), (dict(lse=A + 2), ALIGN, "4-byte"), (dict(wsb=100), SMALL, "workspace"),
     (dict(ws=None), SMALL, "workspace"), (dict(ws=A + 16), ALIGN, "256-byte"), (dict(B=0), OK, ""),
-    (dict(B=0, q=None, table=None, ws=None), OK, ""),
+    (dict(B=0, q=None, table=None, ws=None), OK, ""), (dict(B=65535, Hq=1 << 20), INVALID, "too many"),
 ])
 def test_attention_refusals(L, kw, status, needle):
     a = dict(q=A, table=A, ld=100, pages=100, lengths=A, B=2, Hq=8, scale=0.1, window=0, out=A, lse=A, ws=A, wsb=1 << 30)

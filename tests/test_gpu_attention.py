@@ -41,7 +41,8 @@ def strided(t, pad, dtype=None):
 @pytest.mark.parametrize("T,N,dt,res,pad", [
     (1, 4096, BF, True, 0), (3, 5120, HF, True, 8), (2, 8, BF, False, 0), (5, 64, HF, True, 0), (4, 1040, BF, True, 16),
     (1, 1, BF, True, 0), (3, 7, HF, False, 3), (2, 1041, BF, True, 1), (2, 32768, HF, True, 0), (2, 32776, BF, True, 0),
-    (700, 136, BF, True, 0), (2, 16384, BF, False, 0),
+    (700, 136, BF, True, 0), (2, 16384, BF, False, 0), (37, 128, HF, True, 8), (1, 120, BF, False, 0), (9, 512, BF, True, 0),
+    (300, 520, HF, True, 0), (300, 16392, BF, True, 0), (260, 8192, HF, False, 0),
 ])
 @pytest.mark.parametrize("fp8", [False, True])
 def test_norm(T, N, dt, res, pad, fp8):
@@ -69,6 +70,23 @@ def test_norm(T, N, dt, res, pad, fp8):
     v = y / s[:, None]   # off by the norm's error and one reciprocal and product
     bound = np.abs(v) * (2.0 ** -4 * (1 + 2 * rel) + rel + 4 * ref.U32) + 2.0 ** -10
     assert np.all(np.abs(ref.f64(got[0].float()) - v) <= bound)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_norm_beyond_the_caches(fp8):
+    """A call that moves more than 256 MB takes the streaming form: the same bits as its rows in a smaller call."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    T, N = 6000, 8192
+    x = torch.randn((T, N), generator=g, device=DEV).to(BF)
+    r = torch.randn((T, N), generator=g, device=DEV).to(BF)
+    w = torch.rand(N, generator=g, device=DEV).to(BF)
+    call = nv.rms_norm_fp8 if fp8 else nv.rms_norm
+    big = call(x, w, residual=r)
+    for lo in (0, 2999, T - 300):
+        small = call(x[lo:lo + 300], w, residual=r[lo:lo + 300])
+        for a, b in zip(big, small):
+            assert torch.equal(a[lo:lo + 300].contiguous().view(torch.uint8), b.view(torch.uint8))
 
 
 @pytest.mark.parametrize("N", [4096, 77])

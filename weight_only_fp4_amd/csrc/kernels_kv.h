@@ -156,11 +156,12 @@ __device__ __forceinline__ void kv_store16(const KvSide& side, const KvShape& sh
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxPairs = 128;   // R <= 256
+constexpr int kRopeMaxTokens = 8;    // of a workgroup
 // A unit's eight (cos, sin) pairs take 64 bytes of LDS; units start 80 bytes
 // apart, which spreads the eight units of a 128-column row over all banks.
 constexpr int kRopeUnitWords = 20;
 
-// Workgroup: TB tokens (blockIdx.x) and every gridDim.y-th run of 256 units
+// Workgroup: TB <= kRopeMaxTokens tokens (blockIdx.x) and every gridDim.y-th run of 256 units
 // of them.  First the tokens' (cos, sin) pairs go to LDS, one per thread and
 // round; then each thread takes 16 values at a time: 8 rotated pairs (halves:
 // columns 8 u .. and R / 2 + 8 u ..; neighbours: 16 u ..) or 16 columns that
@@ -171,7 +172,7 @@ constexpr int kRopeUnitWords = 20;
 // and a whole NVFP4 group within two lanes.
 template <int FMT, bool F16, bool NEIGHBOURS>
 __global__ void __launch_bounds__(kRopeThreads) k_rope_append(AppendArgs a, int TB) {
-    __shared__ __attribute__((aligned(16))) float s_cs[4 * (kRopeMaxPairs / 8) * kRopeUnitWords];
+    __shared__ __attribute__((aligned(16))) float s_cs[kRopeMaxTokens * (kRopeMaxPairs / 8) * kRopeUnitWords];
     const int64_t t0 = (int64_t)blockIdx.x * TB;
     const int nt = a.T - t0 < TB ? (int)(a.T - t0) : TB;
     const int half = a.rope.R >> 1, ru = a.rope.R >> 4, U = a.D >> 4;

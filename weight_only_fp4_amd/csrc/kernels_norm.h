@@ -26,25 +26,88 @@ struct NormArgs {
 
 constexpr int kNormMaxWaves = 16;
 
-// Sum over the wave (every lane gets it): five DPP-free shuffles.
-__device__ __forceinline__ float wave_sum(float v) {
+// Sum and maximum over aligned groups of L lanes (every lane gets it).
+template <int L = 64>
+__device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+    for (int d = L / 2; d >= 1; d >>= 1) v += __shfl_xor(v, d);
     return v;
 }
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+template <int L = 64>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
 #pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) {
+    for (int d = L / 2; d >= 1; d >>= 1) {
         const uint32_t o = __shfl_xor(v, d);
         v = o > v ? o : v;
     }
     return v;
 }
 
+// A 16-byte piece, streamed past the caches (PAST) or not.
+template <bool PAST>
+__device__ __forceinline__ uint4 norm_load(const uint16_t* p) {
+    if constexpr (PAST) return load_stream_u4(reinterpret_cast<const uint8_t*>(p));
+    else return *reinterpret_cast<const uint4*>(p);
+}
+// h of a 16-byte piece (x plus the residual's, rounded) as fp32; stored if asked for.
+template <bool F16>
+__device__ __forceinline__ void norm_sum8(const NormArgs& a, int64_t t, int p, uint4 xv, uint4 rv, float (&f)[8]) {
+    unpack8<F16>(xv, f);
+    if (a.r) {
+        float rf[8];
+        unpack8<F16>(rv, rf);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] += rf[e];
+        const uint4 h = pack8<F16>(f);
+        if (a.h) *reinterpret_cast<uint4*>(a.h + t * a.ld_h + p * 8) = h;
+        unpack8<F16>(h, f);
+    }
+}
+
+// Rows of at most 8 L values: L lanes a row, no workgroup-wide step.
+template <bool F16, bool F8, int L>
+__global__ void __launch_bounds__(256) k_rms_norm_short(NormArgs a) {
+    const int p = threadIdx.x & (L - 1);
+    const int64_t row = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+    const bool in = row < a.T && p < (a.N >> 3);
+    const int64_t t = row < a.T ? row : 0;
+    float f[8] = {};
+    uint4 wv = make_uint4(0u, 0u, 0u, 0u);
+    if (in) {
+        wv = *reinterpret_cast<const uint4*>(a.w + p * 8);
+        uint4 rv = wv;
+        if (a.r) rv = *reinterpret_cast<const uint4*>(a.r + t * a.ld_r + p * 8);
+        norm_sum8<F16>(a, t, p, *reinterpret_cast<const uint4*>(a.x + t * a.ld_x + p * 8), rv, f);
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(f[e], f[e], sum);
+    sum = lanes_sum<L>(sum);
+    const float inv = rsqrtf(sum / (float)a.N + a.eps);
+    float wf[8];
+    unpack8<F16>(wv, wf);
+    uint32_t top = 0u;   // largest |y| as bits: a NaN's are above infinity's, so it is kept
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        f[e] = f[e] * inv * wf[e];
+        const uint32_t u = __float_as_uint(f[e]) & 0x7FFFFFFFu;
+        top = in && u > top ? u : top;
+    }
+    if constexpr (!F8) {
+        if (in) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + t * a.ld_y + p * 8) = pack8<F16>(f);
+    } else {
+        const float scale = norm_row_scale(__uint_as_float(lanes_max<L>(top)));
+        if (in) {
+            if (p == 0) a.scales[t] = scale;
+            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.y) + t * a.ld_y + p * 8) = e4m3_pack8(f, __fdiv_rn(1.0f, scale));
+        }
+    }
+}
+
 // One workgroup per row, the row held in registers (V 16-byte pieces a
 // thread): one pass over HBM.  N, the leading dimensions and the pointers
 // keep 16-byte alignment (checked on the host).
-template <bool F16, bool F8, int V>
+template <bool F16, bool F8, int V, bool PAST>
 __global__ void __launch_bounds__(64 * kNormMaxWaves) k_rms_norm(NormArgs a) {
     __shared__ float s_sum[kNormMaxWaves];
     __shared__ uint32_t s_max[kNormMaxWaves];
@@ -58,8 +121,8 @@ __global__ void __launch_bounds__(64 * kNormMaxWaves) k_rms_norm(NormArgs a) {
     for (int i = 0; i < V; ++i) {
         const int p = tid + i * threads;
         if (p < pieces) {
-            xv[i] = *reinterpret_cast<const uint4*>(a.x + t * a.ld_x + p * 8);
-            if (a.r) rv[i] = *reinterpret_cast<const uint4*>(a.r + t * a.ld_r + p * 8);
+            xv[i] = norm_load<PAST>(a.x + t * a.ld_x + p * 8);
+            if (a.r) rv[i] = norm_load<PAST>(a.r + t * a.ld_r + p * 8);
             wv[i] = *reinterpret_cast<const uint4*>(a.w + p * 8);
         }
     }
@@ -67,21 +130,12 @@ __global__ void __launch_bounds__(64 * kNormMaxWaves) k_rms_norm(NormArgs a) {
     for (int i = 0; i < V; ++i) {
         const int p = tid + i * threads;
         if (p < pieces) {
-            unpack8<F16>(xv[i], f[i]);
-            if (a.r) {
-                float rf[8];
-                unpack8<F16>(rv[i], rf);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[i][e] += rf[e];
-                const uint4 h = pack8<F16>(f[i]);
-                if (a.h) *reinterpret_cast<uint4*>(a.h + t * a.ld_h + p * 8) = h;
-                unpack8<F16>(h, f[i]);
-            }
+            norm_sum8<F16>(a, t, p, xv[i], rv[i], f[i]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(f[i][e], f[i][e], sum);
         }
     }
-    sum = wave_sum(sum);
+    sum = lanes_sum(sum);
     if (waves > 1) {
         if ((tid & 63) == 0) s_sum[tid >> 6] = sum;
         __syncthreads();
@@ -104,12 +158,11 @@ __global__ void __launch_bounds__(64 * kNormMaxWaves) k_rms_norm(NormArgs a) {
                     top = u > top ? u : top;
                 }
             }
-            if constexpr (!F8)
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + t * a.ld_y + p * 8) = pack8<F16>(f[i]);
+            if constexpr (!F8) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + t * a.ld_y + p * 8) = pack8<F16>(f[i]);
         }
     }
     if constexpr (F8) {
-        top = wave_max_u32(top);
+        top = lanes_max(top);
         if (waves > 1) {
             if ((tid & 63) == 0) s_max[tid >> 6] = top;
             __syncthreads();
@@ -149,7 +202,7 @@ __global__ void __launch_bounds__(256) k_rms_norm_any(NormArgs a) {
         const float f = act_to_f32<F16>(v);
         sum = __builtin_fmaf(f, f, sum);
     }
-    sum = wave_sum(sum);
+    sum = lanes_sum(sum);
     if ((tid & 63) == 0) s_sum[tid >> 6] = sum;
     __syncthreads();
     sum = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
@@ -168,7 +221,7 @@ __global__ void __launch_bounds__(256) k_rms_norm_any(NormArgs a) {
             const uint32_t u = __float_as_uint(value(i)) & 0x7FFFFFFFu;
             top = u > top ? u : top;
         }
-        top = wave_max_u32(top);
+        top = lanes_max(top);
         if ((tid & 63) == 0) s_max[tid >> 6] = top;
         __syncthreads();
         for (int i = 0; i < 4; ++i) top = s_max[i] > top ? s_max[i] : top;

@@ -18,6 +18,13 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 constexpr int64_t kBig = (int64_t)1 << 40;   // strides and row counts stay below: products fit 64 bits
 
+// A launch holds fewer than 2^32 threads.
+nvfp4_status check_launch(const char* fn, int64_t workgroups, int64_t threads) {
+    if (workgroups * threads >= (int64_t)1 << 32)
+        return fail(NVFP4_ERR_INVALID_ARG, "%s: %lld rows of work are too many for one call", fn, (long long)workgroups);
+    return NVFP4_OK;
+}
+
 // ---------------------------------------------------------------- the norm --
 
 template <bool F16, bool F8>
@@ -27,12 +34,33 @@ void launch_norm(const NormArgs& a, bool vec, hipStream_t st) {
         hipLaunchKernelGGL((k_rms_norm_any<F16, F8>), grid, dim3(256), 0, st, a);
         return;
     }
-    // a row's 16-byte pieces over as many waves as it fills, at most 1024 threads
+    // Rows of up to 256 values (heads): 16 or 32 lanes a row, several rows a
+    // workgroup (60000 x 128: 17.1 us with a wave each, 11.4 so; from 512 values
+    // on a wave each is faster, 20000 x 512 13.2 us against 14.2).
     const int pieces = a.N / 8;
-    const int threads = pieces >= 1024 ? 1024 : (pieces + 63) / 64 * 64;
-    if (pieces <= 1024) hipLaunchKernelGGL((k_rms_norm<F16, F8, 1>), grid, dim3(threads), 0, st, a);
-    else if (pieces <= 2048) hipLaunchKernelGGL((k_rms_norm<F16, F8, 2>), grid, dim3(threads), 0, st, a);
-    else hipLaunchKernelGGL((k_rms_norm<F16, F8, 4>), grid, dim3(threads), 0, st, a);
+    if (pieces <= 16) {
+        hipLaunchKernelGGL((k_rms_norm_short<F16, F8, 16>), dim3((unsigned)((a.T + 15) / 16)), dim3(256), 0, st, a);
+        return;
+    }
+    if (pieces <= 32) {
+        hipLaunchKernelGGL((k_rms_norm_short<F16, F8, 32>), dim3((unsigned)((a.T + 7) / 8)), dim3(256), 0, st, a);
+        return;
+    }
+    // Longer ones: a workgroup a row, one piece a thread while the rows leave
+    // compute units free (a row's latency counts: 1 x 4096 3.5 us against 3.9
+    // with two pieces), two from there on (half the waves to start for the
+    // same loads in flight: 8192 x 5120 to 8 bits 59 -> 49 us), four where a
+    // row needs them.  Calls that move more than the 256 MB Infinity Cache
+    // holds read past it (8192 x 5120, 16 bits: 60 -> 54 us; 2048 x 4096, whose
+    // 67 MB it does hold, would lose 25 %).
+    const int V = pieces > 2048 ? 4 : (pieces > 1024 || a.T >= 256 ? 2 : 1);
+    const int threads = ((pieces + V - 1) / V + 63) / 64 * 64;
+    const bool past = a.T * a.N * (2 + (a.r ? 2 : 0) + (a.h ? 2 : 0) + (F8 ? 1 : 2)) > (int64_t)256 << 20;
+    if (V == 1) hipLaunchKernelGGL((k_rms_norm<F16, F8, 1, false>), grid, dim3(threads), 0, st, a);
+    else if (V == 2 && past) hipLaunchKernelGGL((k_rms_norm<F16, F8, 2, true>), grid, dim3(threads), 0, st, a);
+    else if (V == 2) hipLaunchKernelGGL((k_rms_norm<F16, F8, 2, false>), grid, dim3(threads), 0, st, a);
+    else if (past) hipLaunchKernelGGL((k_rms_norm<F16, F8, 4, true>), grid, dim3(threads), 0, st, a);
+    else hipLaunchKernelGGL((k_rms_norm<F16, F8, 4, false>), grid, dim3(threads), 0, st, a);
 }
 
 constexpr int64_t kNormVecMax = 1024 * 8 * 4;
@@ -134,13 +162,25 @@ void launch_append_fmt(const AppendArgs& a, int TB, dim3 grid, bool f16, bool nb
 }
 
 void launch_append(const AppendArgs& a, int format, bool f16, bool nb, hipStream_t st) {
-    // Four tokens a workgroup share a round of sines where that still leaves
-    // two workgroups per compute unit; with fewer tokens each gets its own, and
-    // a token's units are spread over workgroups (one round of 256 units each).
+    // A workgroup takes 256 units at a time.  With many tokens it gets the
+    // fewest of them (up to eight) whose units fill its rounds to 90 %, or the
+    // best filling there is (5003 tokens of 16 heads of 80: three, 240 units);
+    // with fewer than two workgroups per compute unit each token gets its own,
+    // and its units are spread over workgroups, a round each.
     const int64_t units = (int64_t)(a.Hq + 2 * a.Hk) * (a.D / 16);
-    const int TB = a.T >= 4 * 512 ? 4 : 1;
+    int TB = 1;
+    if (a.T >= 1024) {
+        double best = 0.;
+        for (int n = 1; n <= kRopeMaxTokens && a.T / n >= 512 && best < 0.9; ++n) {
+            const double fill = (double)(n * units) / (double)((n * units + kRopeThreads - 1) / kRopeThreads * kRopeThreads);
+            if (fill > best) {
+                best = fill;
+                TB = n;
+            }
+        }
+    }
     const int64_t rounds = (TB * units + kRopeThreads - 1) / kRopeThreads;
-    int64_t gy = TB == 4 ? 1 : (512 + a.T - 1) / a.T;
+    int64_t gy = a.T >= 1024 ? 1 : (512 + a.T - 1) / a.T;
     if (gy > rounds) gy = rounds;
     const dim3 grid((unsigned)((a.T + TB - 1) / TB), (unsigned)gy);
     if (format == kKv16) launch_append_fmt<kKv16>(a, TB, grid, f16, nb, st);
@@ -193,6 +233,8 @@ nvfp4_status nvfp4_rms_norm(const void* x, int64_t ld_x, const void* residual, i
                      (!h || ld_h % 8 == 0) && aligned(x, 16) && aligned(residual, 16) && aligned(weight, 16) &&
                      aligned(h, 16) && aligned(y, scales ? 8 : 16);
     hipStream_t st = static_cast<hipStream_t>(stream);
+    const nvfp4_status sized = check_launch(fn, T, !vec ? 256 : N <= 128 ? 16 : N <= 256 ? 32 : 1024);
+    if (sized != NVFP4_OK) return sized;
     if (f16) scales ? launch_norm<true, true>(a, vec, st) : launch_norm<true, false>(a, vec, st);
     else scales ? launch_norm<false, true>(a, vec, st) : launch_norm<false, false>(a, vec, st);
     return launched(fn);
@@ -222,6 +264,8 @@ nvfp4_status nvfp4_rope_apply(const nvfp4_rope* rope, const void* x, int64_t x_t
     a.Hq = (int)H;
     a.T = T;
     a.D = (int)D;
+    s = check_launch(fn, T, kRopeThreads);
+    if (s != NVFP4_OK) return s;
     launch_append(a, kKv16, f16 != 0, rope->neighbours != 0, static_cast<hipStream_t>(stream));
     return launched(fn);
 }
@@ -270,6 +314,8 @@ nvfp4_status nvfp4_kv_append(const nvfp4_kv_cache* cache, const nvfp4_rope* rope
     a.shape = c.shape;
     a.T = T;
     a.D = c.shape.D;
+    s = check_launch(fn, T, kRopeThreads);
+    if (s != NVFP4_OK) return s;
     launch_append(a, c.format, f16 != 0, rope && rope->neighbours != 0, static_cast<hipStream_t>(stream));
     return launched(fn);
 }
@@ -301,7 +347,8 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const int32_t* slots, vo
     a.T = T;
     const int64_t threads = T * 2 * c.shape.heads * (c.shape.D / 16);
     const int64_t groups = (threads + 255) / 256;
-    if (groups >= (int64_t)1 << 31) return fail(NVFP4_ERR_INVALID_ARG, "%s: T = %lld rows of this cache are too many for one call", fn, (long long)T);
+    s = check_launch(fn, groups, 256);
+    if (s != NVFP4_OK) return s;
     const dim3 grid((unsigned)groups);
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (c.format == kKv16) launch_read<kKv16>(a, f16 != 0, grid, st);
@@ -322,6 +369,8 @@ nvfp4_status check_attn_sizes(const char* fn, int64_t B, int64_t Hq, int64_t hea
     if (heads * ((Hq / heads + kAttnHeads - 1) / kAttnHeads) > 65535)
         return fail(NVFP4_ERR_INVALID_ARG, "%s: Hq = %lld over %lld key-value heads is too many heads", fn, (long long)Hq, (long long)heads);
     if (D < 16 || D > 256 || D % 16 != 0) return fail(NVFP4_ERR_INVALID_ARG, "%s: D = %lld must be a multiple of 16 up to 256", fn, (long long)D);
+    const nvfp4_status sized = check_launch(fn, B * heads * ((Hq / heads + kAttnHeads - 1) / kAttnHeads), kAttnThreads);
+    if (sized != NVFP4_OK) return sized;
     if (max_tokens < 0 || max_tokens >= (int64_t)1 << 30)
         return fail(NVFP4_ERR_INVALID_ARG, "%s: %lld tokens: the table must hold fewer than 2^30", fn, (long long)max_tokens);
     return NVFP4_OK;
