@@ -266,6 +266,13 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
         b = __builtin_amdgcn_readfirstlane(lo);
     }
 
+    // Of the waves of a SIMD the oldest issues first, so that a younger one's
+    // work is largely left for the end, when it has the SIMD to itself and
+    // cannot fill it.  Every wave therefore gives up a step of priority with
+    // each quarter of its stretch: those behind go first.
+    __builtin_amdgcn_s_setprio(3);
+    const int quarter = (p_end - p_begin + 3) / 4;
+    int prio_place = p_begin + quarter, prio = 3;
     for (int place = p_begin; place < p_end;) {
         // ---- the segment: units [unit0, unit1) of pair (b, ph)
         int first, len, ph, units, unit0, unit1;
@@ -546,6 +553,14 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
             }
         };
 
+        auto step_down = [&](int t) {   // before the tile at t
+            if (pair_begin + (t - base_t) / kAttnUnit < prio_place) return;
+            prio_place += quarter;
+            if (--prio == 2) __builtin_amdgcn_s_setprio(2);
+            else if (prio == 1) __builtin_amdgcn_s_setprio(1);
+            else __builtin_amdgcn_s_setprio(0);
+        };
+
         // ---- the tiles.  Loads run one tile ahead where the registers hold
         // two tiles (past the end they read page 0's rows, which no one uses).
         int t0 = base_t + unit0 * kAttnUnit + w * kAttnTile;
@@ -587,6 +602,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
             }
             if constexpr (AHEAD) {
                 for (;;) {
+                    step_down(t0);
                     pg = pages_of(t0 + 2 * kAttnUnit);
                     load_tile(x1, t0 + kAttnUnit, pn);
                     work_tile(x0);
@@ -600,6 +616,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
                 }
             } else {
                 for (;;) {
+                    step_down(t0);
                     work_tile(x0);
                     t0 += kAttnUnit;
                     if (t0 >= t_stop) break;
