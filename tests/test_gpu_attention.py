@@ -420,6 +420,61 @@ def test_attention_window(kind):
         p.check(p.run(window=window), window=window)
 
 
+@pytest.mark.parametrize("kind", ["same", "fp8", "fp4"])
+@pytest.mark.parametrize("most,D", [(900, 64), (150, 128)])
+def test_attention_many_ragged_sequences(most, D, kind):
+    """More pairs than workgroups: a stretch ends one pair, holds whole ones and begins another."""
+    say(f"130 sequences of up to {most}, D={D}, {kind}")
+    lengths = torch.randint(0, most + 1, (130,), generator=gen(most)).tolist()
+    p = Paged(lengths, 12, 4, D, 16, kind, BF)
+    p.check(p.run())
+
+
+@pytest.mark.parametrize("B", [2048, 2049, 2300])
+def test_attention_more_sequences_than_are_counted(B):
+    say(f"{B} sequences")
+    lengths = torch.randint(0, 200, (B,), generator=gen(B)).tolist()
+    p = Paged(lengths, 2, 1, 64, 16, "fp4", HF)
+    p.check(p.run())
+
+
+@pytest.mark.parametrize("kind", ["same", "fp8", "fp4"])
+@pytest.mark.parametrize("lengths,Hq,Hk", [([60000] + list(range(7)), 1, 1), ([3, 20000, 0], 16, 1), ([5, 5, 30000], 34, 2)])
+def test_attention_one_long_sequence_among_short_ones(lengths, Hq, Hk, kind):
+    """The long pair's partial results are more than a join's one round."""
+    say(f"{lengths} {Hq}x{Hk} {kind}")
+    p = Paged(lengths, Hq, Hk, 64, 32, kind, BF)
+    p.check(p.run())
+
+
+@pytest.mark.parametrize("kind", ["same", "fp8", "fp4"])
+@pytest.mark.parametrize("lengths", [[512], [513], [640], [641], [2016], [2048], [2049], [2176], [700, 512, 1000, 31], [4096]])
+def test_attention_lengths_around_the_rule_of_the_split(lengths, kind):
+    say(f"{lengths} {kind}")
+    p = Paged(lengths, 8, 2, 128, 16, kind, HF)
+    p.check(p.run())
+    room = torch.full((len(lengths), 5000), -1, dtype=torch.int32)   # a table for much longer sequences
+    room[:, :p.table.shape[1]] = p.table
+    p.check(p.run(table=room))
+
+
+@pytest.mark.parametrize("kind", ["same", "fp8", "fp4"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_pages_of_48_in_a_permuted_cache(D, kind):
+    p = Paged([500, 47, 48, 49, 0, 1300], 10, 2, D, 48, kind, BF, permuted=True)
+    for window in (0, 50, 400):
+        say(f"pages of 48, D={D}, {kind}, window {window}")
+        p.check(p.run(window=window), window=window)
+
+
+@pytest.mark.parametrize("kind", ["same", "fp8", "fp4"])
+def test_attention_scales_of_any_sign(kind):
+    p = Paged([700, 1, 33], 8, 2, 128, 16, kind, BF)
+    for scale in (-0.07, 0.0, 0.5):
+        say(f"softmax scale {scale}, {kind}")
+        p.check(p.run(scale=scale), scale=scale)
+
+
 def test_attention_long_split_and_a_reused_workspace():
     """One workspace through calls of different sizes (the partial results of one lie where another's would start)."""
     p = Paged([40000], 8, 2, 128, 64, "fp8", BF)

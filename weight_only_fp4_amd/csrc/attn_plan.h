@@ -31,7 +31,7 @@ inline AttnShape attn_shape(int64_t B, int64_t Hk, int64_t G, int64_t D, int64_t
     s.split = B <= kAttnScan && places >= 8 && places < ((int64_t)1 << 31);
     s.workgroups = s.pairs;
     if (s.split) {
-        int64_t each = units / 4 + 1;
+        int64_t each = units + 1;
         if (each > kAttnPairSplits) each = kAttnPairSplits;
         s.workgroups = s.pairs * each < kAttnMaxWorkgroups ? s.pairs * each : kAttnMaxWorkgroups;
     }
@@ -40,8 +40,7 @@ inline AttnShape attn_shape(int64_t B, int64_t Hk, int64_t G, int64_t D, int64_t
 }
 
 // Defined by attn.hip, once per cache format (0 bf16, 1 fp16, 2 E4M3, 3
-// NVFP4): fast pages (kernels_attn.h), the number of workgroups a split call
-// fills the chip with, and the launch.
+// NVFP4): the launch, `fast` as kernels_attn.h has it.
 void launch_attn_bf16(const AttnArgs& a, bool fast, int64_t workgroups, hipStream_t st);
 void launch_attn_f16(const AttnArgs& a, bool fast, int64_t workgroups, hipStream_t st);
 void launch_attn_e4m3(const AttnArgs& a, bool fast, int64_t workgroups, hipStream_t st);

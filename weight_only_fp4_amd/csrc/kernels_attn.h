@@ -42,6 +42,8 @@ constexpr int kAttnScan = 2048;                             // sequences whose u
 constexpr int kAttnMaxWorkgroups = 512;                     // of a split call
 constexpr int kAttnPairSplits = 64;                         // at most this many workgroups per pair on average: the
                                                             // last of them joins what they leave
+constexpr unsigned kAttnWhole = 6;                          // pairs of fewer places are not split
+constexpr int kAttnJoin = 16;                               // partial results a join fetches at a time
 constexpr int kAttnOutCols = 64;                            // columns of the accumulators that go through LDS at a time
 
 // Read-only memory at a uniform address (scalar loads), and rows of the cache.
@@ -77,7 +79,6 @@ __device__ __forceinline__ f16x2v f16_group_scale(uint32_t pair_bytes, bool seco
     const uint32_t h = second ? (p >> 16) : (p & 0xFFFFu);
     return __builtin_bit_cast(f16x2v, h | (h << 16));
 }
-
 
 // Maximum over the four lanes of a query head (lanes 16 apart).
 __device__ __forceinline__ float attn_head_max(float v) {
@@ -130,13 +131,20 @@ __device__ __forceinline__ void attn_load(AttnRow p, uint32_t* d) {
 // each pair with one more place in front for what a pair costs besides its
 // tokens, and workgroup j of N takes the places from floor(j P / N) to
 // floor((j + 1) P / N) of all P, so every compute unit gets the same work
-// whatever the lengths are.  N is a multiple of the pairs while that leaves
-// four places a workgroup (pairs of equal lengths are then split at equal
-// places and short ones not at all), and at most the grid.  A stretch is a few
-// segments, each a run of units of one pair; a segment that is not the
-// whole pair leaves a partial result, and the workgroup that arrives last at
-// a pair adds the partial results in their order (so the result does not
-// depend on timing).
+// whatever the lengths are.  N is at most the grid, and a multiple of the pairs
+// (equal lengths are then split at equal places): with p places a pair on
+// average
+//   p < 6      one workgroup a pair: a join costs more than four units do
+//              (2 x 300 tokens: 9.3 us, halved 10.6);
+//   p <= 17    p workgroups while no compute unit gets a second one, so each
+//              works on one unit and the join takes one round trip (1 x 1024
+//              tokens: 9.4 us, p / 2 workgroups 11.4, p / 4 13.5);
+//   else       p / 2 (1 x 8192 tokens: 15.9 us, p / 4 17.3, p 19.7: the join
+//              of more than 16 partial results takes several).
+// A stretch is a few segments, each a run of units of one pair; a segment that
+// is not the whole pair leaves a partial result, and the workgroup that arrives
+// last at a pair adds the partial results in their order (so the result does
+// not depend on timing).
 //
 // A workgroup's waves take the segment's tiles of 32 tokens in turn, each with
 // its own running maximum, sum and accumulators: the loop has no barrier.  A
@@ -250,8 +258,11 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
         }
         __syncthreads();
         places = (unsigned)__builtin_amdgcn_readfirstlane(s_pre[a.B]) * (unsigned)HT;   // below 2^31
-        const unsigned pairs = (unsigned)(a.B * HT), each = places / (4u * pairs);
-        groups = (int)(pairs * (each < 1 ? 1 : (each > kAttnPairSplits ? kAttnPairSplits : each)));
+        const unsigned pairs = (unsigned)(a.B * HT), per = places / pairs;
+        unsigned each = per < kAttnWhole ? 1u : per / 2;
+        if (per >= kAttnWhole && per <= kAttnJoin + 1 && places <= 256) each = per;
+        if (each > kAttnPairSplits) each = kAttnPairSplits;
+        groups = (int)(pairs * each);
         groups = groups < (int)gridDim.x ? groups : (int)gridDim.x;
         if ((int)blockIdx.x >= groups) return;
         p_begin = quotient((int64_t)blockIdx.x * places, groups);
@@ -722,32 +733,31 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
             return __hip_atomic_load(reinterpret_cast<const uint64_t*>(from), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         };
         const int half = D / 2;
-        constexpr int kJoinLoads = 16;
-        uint64_t v[kJoinLoads];
+        uint64_t v[kAttnJoin];
         auto fetch = [&](const float* from, int x0) {   // partial results x0 .. (the last one again past the end)
             from += (int64_t)x0 * 2 * part_floats + (x0 == 0 ? second : 0);
 #pragma unroll
-            for (int x = 0; x < kJoinLoads; ++x) {
+            for (int x = 0; x < kAttnJoin; ++x) {
                 v[x] = load2(from);
                 from += x0 + x + 1 < parts ? 2 * part_floats - (x0 + x == 0 ? second : 0) : 0;
             }
         };
-        if (parts <= kJoinLoads) {
+        if (parts <= kAttnJoin) {
             // few: each thread fetches its head's (maximum, sum) pairs with its
             // columns and works the factors out itself, one round trip in all
             for (int i = threadIdx.x; i < nh * half; i += kAttnThreads) {
                 const int h = i / half, d = (i - h * half) * 2;
-                uint64_t ml[kJoinLoads];
+                uint64_t ml[kAttnJoin];
                 fetch(parts0 + hp * D + 2 * h, 0);
 #pragma unroll
-                for (int x = 0; x < kJoinLoads; ++x) ml[x] = v[x];
+                for (int x = 0; x < kAttnJoin; ++x) ml[x] = v[x];
                 fetch(parts0 + h * D + d, 0);
                 float mm = __uint_as_float((uint32_t)ml[0]);
 #pragma unroll
-                for (int x = 1; x < kJoinLoads; ++x) mm = fmaxf(mm, __uint_as_float((uint32_t)ml[x]));
+                for (int x = 1; x < kAttnJoin; ++x) mm = fmaxf(mm, __uint_as_float((uint32_t)ml[x]));
                 float ll = 0.f, o0 = 0.f, o1 = 0.f;
 #pragma unroll
-                for (int x = 0; x < kJoinLoads; ++x) {
+                for (int x = 0; x < kAttnJoin; ++x) {
                     const float mx = __uint_as_float((uint32_t)ml[x]);
                     const float f = x >= parts || mx == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mx - mm);
                     if (x < parts) {
@@ -806,13 +816,13 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
             const int h = i / half;
             for (int x0 = 0;;) {
 #pragma unroll
-                for (int x = 0; x < kJoinLoads; ++x) {
+                for (int x = 0; x < kAttnJoin; ++x) {
                     if (x0 + x >= parts) break;
                     const float f = s_f[(x0 + x) * nh + (h < nh ? h : 0)];
                     o0 = __builtin_fmaf(f, __uint_as_float((uint32_t)v[x]), o0);
                     o1 = __builtin_fmaf(f, __uint_as_float((uint32_t)(v[x] >> 32)), o1);
                 }
-                x0 += kJoinLoads;
+                x0 += kAttnJoin;
                 if (x0 >= parts) break;
                 fetch(columns(i), x0);
             }
