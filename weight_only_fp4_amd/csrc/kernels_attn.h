@@ -50,12 +50,6 @@ constexpr int kAttnOutCols = 64;                            // columns of the ac
 typedef const __attribute__((address_space(4))) int32_t* AttnTable;
 typedef const __attribute__((address_space(4))) float* AttnScales;
 typedef const __attribute__((address_space(1))) uint8_t* AttnRow;
-// A row address every lane holds the same value of, kept in scalar registers.
-__device__ __forceinline__ AttnRow attn_row(uint64_t v) {
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
-    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-    return (AttnRow)(((uint64_t)hi << 32) | lo);
-}
 
 // fp16 pair of two E4M3 bytes / two E2M1 codes
 template <bool HI>
@@ -102,6 +96,26 @@ __device__ __forceinline__ float attn_wave_reduce(float v, Op op) {
     return op(v, __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x121, 0xF, 0xF, true)));
 }
 
+// Lane i of four gets the j-th's x[i] as x[j]: the square of four lanes and
+// four registers, transposed.
+__device__ __forceinline__ void attn_quad_transpose(uint32_t& x0, uint32_t& x1, uint32_t& x2, uint32_t& x3, int lane) {
+    const bool b0 = lane & 1, b1 = lane & 2;
+    auto next = [](uint32_t v) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true); };    // lane ^ 1
+    auto other = [](uint32_t v) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true); };   // lane ^ 2
+    // every lane takes part in the exchanges: they stand before the selections
+    const uint32_t n0 = next(x0), n1 = next(x1), n2 = next(x2), n3 = next(x3);
+    const uint32_t y0 = b0 ? n1 : x0, y1 = b0 ? x1 : n0, y2 = b0 ? n3 : x2, y3 = b0 ? x3 : n2;
+    const uint32_t o0 = other(y0), o1 = other(y1), o2 = other(y2), o3 = other(y3);
+    x0 = b1 ? o2 : y0;
+    x2 = b1 ? y2 : o0;
+    x1 = b1 ? o3 : y1;
+    x3 = b1 ? y3 : o1;
+}
+template <int J>
+__device__ __forceinline__ uint32_t attn_quad_lane(uint32_t v) {   // lane J's of each four
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, J * 0x55, 0xF, 0xF, true);
+}
+
 // Streaming loads: the cache's rows are read once.
 template <int BYTES>
 __device__ __forceinline__ void attn_load(AttnRow p, uint32_t* d) {
@@ -117,6 +131,34 @@ __device__ __forceinline__ void attn_load(AttnRow p, uint32_t* d) {
 #pragma unroll
         for (int x = 0; x < BYTES / 16; ++x) {
             const u32x4v t = __builtin_nontemporal_load((const __attribute__((address_space(1))) u32x4v*)p + x);
+            d[4 * x] = t[0];
+            d[4 * x + 1] = t[1];
+            d[4 * x + 2] = t[2];
+            d[4 * x + 3] = t[3];
+        }
+    }
+}
+
+// A row of the cache as a buffer: the scalar base, 32-bit offsets of the lanes,
+// and reads of nothing (zeros come back) where `there` is false.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t attn_buffer(uint64_t base, bool there) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, there ? 1 << 30 : 0, 0x00027000);
+}
+template <int BYTES>
+__device__ __forceinline__ void attn_buffer_load(__amdgpu_buffer_rsrc_t r, uint32_t lane_at, uint32_t at, uint32_t* d) {
+    constexpr int NT = 2;   // streaming
+    typedef unsigned u32x2v __attribute__((ext_vector_type(2)));
+    if constexpr (BYTES == 1) d[0] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r, (int)lane_at, (int)at, NT);
+    else if constexpr (BYTES == 2) d[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)lane_at, (int)at, NT);
+    else if constexpr (BYTES == 4) d[0] = __builtin_amdgcn_raw_buffer_load_b32(r, (int)lane_at, (int)at, NT);
+    else if constexpr (BYTES == 8) {
+        const u32x2v t = __builtin_amdgcn_raw_buffer_load_b64(r, (int)lane_at, (int)at, NT);
+        d[0] = t[0];
+        d[1] = t[1];
+    } else {
+#pragma unroll
+        for (int x = 0; x < BYTES / 16; ++x) {
+            const u32x4v t = __builtin_amdgcn_raw_buffer_load_b128(r, (int)lane_at + x * 16, (int)at, NT);
             d[4 * x] = t[0];
             d[4 * x + 1] = t[1];
             d[4 * x + 2] = t[2];
@@ -171,7 +213,11 @@ __device__ __forceinline__ void attn_load(AttnRow p, uint32_t* d) {
 //   FAST   D is DT and pages are multiples of 16 tokens: a half-tile of 16
 //          tokens lies in one page, so its base is a scalar and the lanes'
 //          offsets never change (tiles begin at multiples of 32 tokens; a
-//          window's first tile masks the tokens before it);
+//          window's first tile masks the tokens before it).  It is read as a
+//          buffer whose size is 0 for a half-tile past the segment's end or
+//          of a page outside the cache: such loads touch no memory (with page
+//          0's rows read in their place, which every wave of the chip did at
+//          its end, 128 x 0..2000 tokens took 63 us instead of 59);
 //   else   any D and page size: the tile's 32 row offsets pass through LDS
 //          (each wave its own, no barrier).
 //
@@ -338,7 +384,6 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
         }
 
         const uint64_t kb = (uint64_t)a.kc.base + hk * a.kc.s_head, vb = (uint64_t)a.vc.base + hk * a.vc.s_head;
-        AttnTable table = (AttnTable)(uint64_t)(a.table + b * a.ld_table);
         auto page_index = [&](int t) { return ps == 1 ? t : (int)(__umulhi((uint32_t)t, a.page_magic) >> a.page_shift); };
         auto in_cache = [&](int p) { return (uint32_t)p < (uint32_t)a.shape.pages; };
 
@@ -354,60 +399,99 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
         // FAST: the lane's offsets inside a half-tile
         const uint32_t k_tok = KV == kKvNvfp4 ? (uint32_t)(D / 2) : (uint32_t)a.kc.s_token;
         const uint32_t v_tok = KV == kKvNvfp4 ? (uint32_t)(D / 2) : (uint32_t)a.vc.s_token;
-        const uint32_t k_lane = c * k_tok + g * KB, v_lane = g * 4 * v_tok + c * VB;
+        // WIDE: of an NVFP4 value row a lane loads the quarter c / 4 of token 4 g +
+        // c % 4, and four lanes then exchange pieces so that each has its columns
+        // of the four tokens: 8 loads a tile instead of 20 with the lane's own
+        // columns, which cost more than the exchange (32 x 8192 tokens: 67 -> 62
+        // us).  A row of 64 columns has only two bytes a lane to exchange.
+        constexpr bool WIDE = FAST && KV == kKvNvfp4 && DT >= 128;
+        const uint32_t k_lane = c * k_tok + g * KB;
+        const uint32_t v_lane = WIDE ? (g * 4 + (c & 3)) * v_tok + (c >> 2) * VB * 4 : g * 4 * v_tok + c * VB;
         const uint32_t ks_lane = c * (D / 16) + (DT == 64 ? g : g * 2);
-        const uint32_t vs_lane = g * 4 * (D / 16) + c * VD / 16;
+        const uint32_t vs_lane = WIDE ? (g * 4 + (c & 3)) * (D / 16) + (c >> 2) * (VD / 4) : g * 4 * (D / 16) + c * VD / 16;
+        // WIDE: picks the lane's group scale of a token pair from both tokens' quarters
+        const uint32_t vs_at = DT == 256 ? c & 3 : (c >> 1) & 1, vs_pair = 0x0C0C0400u + vs_at * 0x0101u;
 
-        // Table entries of the tile at t: FAST its two half-tiles', else the
-        // lane's token's; -1 past the segment's end.
-        struct Pages {
-            int p[2];
-        };
-        auto pages_of = [&](int t) {
-            Pages r;
-            if constexpr (FAST) {
-                r.p[0] = t < t_stop ? table[page_index(t)] : -1;
-                r.p[1] = t + 16 < t_stop ? table[page_index(t + 16)] : -1;
-            } else {
-                r.p[0] = lane < kAttnTile && t + lane < t_stop ? a.table[b * a.ld_table + page_index(t + lane)] : -1;
-                r.p[1] = -1;
-            }
-            return r;
-        };
-        auto load_tile = [&](Tile& x, int t, const Pages& pg) {
-            // tokens of the tile inside [first, t_stop), one bit each
+        auto token_mask = [&](int t) {   // tokens of the tile at t inside [first, t_stop), one bit each
             const int lo = first > t ? first - t : 0, hi = t_stop - t;
             uint32_t valid = hi >= kAttnTile ? 0xFFFFFFFFu : (hi <= 0 ? 0u : (1u << hi) - 1u);
             if (lo > 0) valid = lo >= kAttnTile ? 0u : valid & (0xFFFFFFFFu << lo);
+            return valid;
+        };
+        // FAST: where the rows of the wave's next 32 tiles are: lane 2 i + h holds
+        // the offsets of half-tile h of the i-th (in 16 bytes; `deep`: from its
+        // codes to its group scales, NVFP4), so a tile takes a few lane reads
+        // instead of two table lookups and their 64-bit products.
+        uint32_t at_k = 0, at_v = 0, deep = 0;
+        uint64_t odd = 0, out_of_cache = 0;   // half-tiles that are not whole; whose entry is outside the cache
+        int ahead = -1;                       // the lane's table entry of the 32 tiles after those
+        int turn = 0;                         // lane of the next tile
+        auto lane_token = [&](int t) { return t + (lane >> 1) * kAttnUnit + (lane & 1) * 16; };
+        auto fetch_entries = [&](int t) {
+            const int mine = lane_token(t);
+            ahead = -1;
+            if (mine < t_stop) ahead = a.table[b * a.ld_table + page_index(mine)];
+        };
+        auto place_rows = [&](int t) {   // of the 32 tiles from the one at t
+            const int mine = lane_token(t);
+            const bool ok = in_cache(ahead);
+            const int64_t page = ok ? ahead : 0, tok = ok ? mine - page_index(mine) * ps : 0;
+            at_k = (uint32_t)((page * a.kc.s_page + tok * k_tok) >> 4);
+            at_v = (uint32_t)((page * a.vc.s_page + tok * v_tok) >> 4);
+            if constexpr (KV == kKvNvfp4) deep = (uint32_t)(scales_at - tok * (D / 2 - D / 16));
+            out_of_cache = __ballot(!ok);
+            odd = __ballot(!ok || mine < first || mine + 16 > t_stop);
+            turn = 0;
+            if (t + 32 * kAttnUnit < t_stop) fetch_entries(t + 32 * kAttnUnit);
+        };
+        auto load_tile = [&](Tile& x, int t) {
             if constexpr (FAST) {
+                uint32_t valid = 0xFFFFFFFFu;   // tokens of the tile inside [first, t_stop) and the cache, one bit each
+                if ((odd >> turn) & 3u) {
+                    valid = token_mask(t);
+                    if ((out_of_cache >> turn) & 1u) valid &= 0xFFFF0000u;
+                    if ((out_of_cache >> turn) & 2u) valid &= 0x0000FFFFu;
+                }
+                x.valid = valid;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int th = t + 16 * h;
-                    // an entry outside the cache: masked, and page 0's first rows are read in its place
-                    const bool ok = in_cache(pg.p[h]);
-                    if (!ok) valid &= h == 0 ? 0xFFFF0000u : 0x0000FFFFu;
-                    const int page = ok ? pg.p[h] : 0, tok = ok ? th - page_index(th) * ps : 0;
-                    const AttnRow kp = attn_row(kb + page * a.kc.s_page + (int64_t)tok * k_tok);
-                    const AttnRow vp = attn_row(vb + page * a.vc.s_page + (int64_t)tok * v_tok);
+                    const bool there = !((out_of_cache >> (turn + h)) & 1u);
+                    const auto kr = attn_buffer(kb + ((uint64_t)(uint32_t)__builtin_amdgcn_readlane(at_k, turn + h) << 4), there);
+                    const auto vr = attn_buffer(vb + ((uint64_t)(uint32_t)__builtin_amdgcn_readlane(at_v, turn + h) << 4), there);
 #pragma unroll
-                    for (int p = 0; p < KP; ++p) attn_load<KB>(kp + (k_lane + p * 64), x.kraw[h][p]);
+                    for (int p = 0; p < KP; ++p) attn_buffer_load<KB>(kr, k_lane + p * 64, 0u, x.kraw[h][p]);
+                    const uint32_t far = KV == kKvNvfp4 ? __builtin_amdgcn_readlane(deep, turn + h) : 0u;
                     if constexpr (KV == kKvNvfp4) {
-                        const AttnRow ksp = attn_row(kb + page * a.kc.s_page + scales_at + (int64_t)tok * (D / 16));
 #pragma unroll
-                        for (int p = 0; p < KP; ++p) attn_load<DT == 64 ? 1 : 2>(ksp + (ks_lane + p * 8), &x.ksc[h][p]);
+                        for (int p = 0; p < KP; ++p) attn_buffer_load<DT == 64 ? 1 : 2>(kr, ks_lane + p * 8, far, &x.ksc[h][p]);
                     }
+                    if constexpr (WIDE) {
+                        uint32_t row[4 * VW];
+                        attn_buffer_load<VB * 4>(vr, v_lane, 0u, row);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) attn_load<VB>(vp + (v_lane + i * v_tok), x.vraw[4 * h + i]);
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int y = 0; y < VW; ++y) x.vraw[4 * h + i][y] = row[i * VW + y];
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) attn_buffer_load<VB>(vr, v_lane + i * v_tok, 0u, x.vraw[4 * h + i]);
+                    }
                     if constexpr (KV == kKvNvfp4) {
-                        const AttnRow vsp = attn_row(vb + page * a.vc.s_page + scales_at + (int64_t)tok * (D / 16));
+                        if constexpr (WIDE) {
+                            attn_buffer_load<VD / 4>(vr, vs_lane, far, &x.vsc[4 * h]);
+                        } else {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) attn_load<1>(vsp + (vs_lane + i * (D / 16)), &x.vsc[4 * h + i]);
+                            for (int i = 0; i < 4; ++i) attn_buffer_load<1>(vr, vs_lane + i * (D / 16), far, &x.vsc[4 * h + i]);
+                        }
                     }
                 }
+                turn += 2;
             } else {
-                const int page = pg.p[0], tok = t + lane - page_index(t + lane) * ps;
+                // `ahead`: the table entry of the lane's token (the first 32 lanes)
+                const int page = ahead, tok = t + lane - page_index(t + lane) * ps;
                 const bool ok = in_cache(page);
-                valid &= (uint32_t)__ballot(ok);
+                x.valid = token_mask(t) & (uint32_t)__ballot(ok);
+                ahead = lane < kAttnTile && t + kAttnUnit + lane < t_stop ? a.table[b * a.ld_table + page_index(t + kAttnUnit + lane)] : -1;
                 if (lane < kAttnTile) {
                     // offsets in units of 16 bytes; a masked row is the head's first in its place
                     s_off[w][0][lane] = ok ? (uint32_t)((page * a.kc.s_page + (KV == kKvNvfp4 ? 0 : tok * a.kc.s_token)) >> 4) : 0u;
@@ -453,7 +537,6 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
                 }
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             }
-            x.valid = valid;
         };
 
         f32x4 acc[VD];
@@ -497,9 +580,13 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
                 for (int i = 0; i < 8; ++i) {
                     const bool ok = (x.valid >> ((i >> 2) * 16 + g * 4 + (i & 3))) & 1u;
                     s[i] = ok ? s[i] : -INFINITY;
-                    if constexpr (KV == kKvNvfp4) x.vsc[i] = ok ? x.vsc[i] : 0u;
+                    // the value row loaded into x.vraw[i]
+                    const bool row_ok = WIDE ? (x.valid >> ((i >> 2) * 16 + g * 4 + (c & 3))) & 1u : ok;
+                    if constexpr (KV == kKvNvfp4) {
+                        if (!WIDE || (i & 3) == 0) x.vsc[i] = row_ok ? x.vsc[i] : 0u;
+                    }
 #pragma unroll
-                    for (int y = 0; y < VW; ++y) x.vraw[i][y] = ok ? x.vraw[i][y] : 0u;
+                    for (int y = 0; y < VW; ++y) x.vraw[i][y] = row_ok ? x.vraw[i][y] : 0u;
                 }
             }
             float top = s[0];
@@ -523,6 +610,23 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
             }
             const uint4 pf = make_uint4(pack_round2<F16>(p[0], p[1]), pack_round2<F16>(p[2], p[3]),
                                         pack_round2<F16>(p[4], p[5]), pack_round2<F16>(p[6], p[7]));
+            uint32_t vs[4];   // NVFP4: group scales of the token pairs
+            if constexpr (KV == kKvNvfp4) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if constexpr (WIDE) {
+#pragma unroll
+                        for (int y = 0; y < VW; ++y)
+                            attn_quad_transpose(x.vraw[4 * h][y], x.vraw[4 * h + 1][y], x.vraw[4 * h + 2][y], x.vraw[4 * h + 3][y], lane);
+                        const uint32_t q = x.vsc[4 * h];
+                        vs[2 * h] = __builtin_amdgcn_perm(attn_quad_lane<1>(q), attn_quad_lane<0>(q), vs_pair);
+                        vs[2 * h + 1] = __builtin_amdgcn_perm(attn_quad_lane<3>(q), attn_quad_lane<2>(q), vs_pair);
+                    } else {
+                        vs[2 * h] = x.vsc[4 * h] | (x.vsc[4 * h + 1] << 8);
+                        vs[2 * h + 1] = x.vsc[4 * h + 2] | (x.vsc[4 * h + 3] << 8);
+                    }
+                }
+            }
             // ---- values, transposed: a dword holds one column of a token pair
 #pragma unroll
             for (int e0 = 0; e0 < VD; e0 += 8) {
@@ -536,7 +640,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
                         const uint32_t ca = x.vraw[2 * i][e0 / 8], cb = x.vraw[2 * i + 1][e0 / 8];
                         const uint32_t even = (ca & 0x0F0F0F0Fu) | ((cb << 4) & 0xF0F0F0F0u);
                         const uint32_t odd = ((ca >> 4) & 0x0F0F0F0Fu) | (cb & 0xF0F0F0F0u);
-                        const f16x2v gs = __builtin_bit_cast(f16x2v, f16_of_e4m3<false>(x.vsc[2 * i] | (x.vsc[2 * i + 1] << 8)));
+                        const f16x2v gs = __builtin_bit_cast(f16x2v, f16_of_e4m3<false>(vs[i]));
                         const uint4 ve = f16_of_nvfp4(even, gs), vo = f16_of_nvfp4(odd, gs);
                         const uint32_t d[8] = {ve.x, vo.x, ve.y, vo.y, ve.z, vo.z, ve.w, vo.w};
 #pragma unroll
@@ -573,15 +677,19 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
         };
 
         // ---- the tiles.  Loads run one tile ahead where the registers hold
-        // two tiles (past the end they read page 0's rows, which no one uses).
+        // two tiles (with the accumulators and q within 200 of 256).  Two ahead
+        // are slower: 131072 tokens (E4M3) 63 us instead of 56.
         int t0 = base_t + unit0 * kAttnUnit + w * kAttnTile;
-        // (two tiles, the accumulators and q within 200 of 256).
         constexpr bool AHEAD = FAST && 2 * (KP * 8 + VW * 8) + VD * 4 + KSTEPS * 4 <= 200;
         if (t0 < t_stop) {
-            Pages pg = pages_of(t0);
-            Pages pn = pages_of(t0 + kAttnUnit);
+            if constexpr (FAST) {
+                fetch_entries(t0);
+                place_rows(t0);
+            } else if (lane < kAttnTile && t0 + lane < t_stop) {
+                ahead = a.table[b * a.ld_table + page_index(t0 + lane)];
+            }
             Tile x0, x1;
-            load_tile(x0, t0, pg);
+            load_tile(x0, t0);
             if constexpr (KV != kKv16) {   // q to fp16, while the first tile is on its way
                 uint32_t top = 0u;
                 float f[KSTEPS][8];
@@ -614,13 +722,12 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
             if constexpr (AHEAD) {
                 for (;;) {
                     step_down(t0);
-                    pg = pages_of(t0 + 2 * kAttnUnit);
-                    load_tile(x1, t0 + kAttnUnit, pn);
+                    load_tile(x1, t0 + kAttnUnit);
                     work_tile(x0);
                     t0 += kAttnUnit;
                     if (t0 >= t_stop) break;
-                    pn = pages_of(t0 + 2 * kAttnUnit);
-                    load_tile(x0, t0 + kAttnUnit, pg);
+                    if (turn == 64) place_rows(t0 + kAttnUnit);
+                    load_tile(x0, t0 + kAttnUnit);
                     work_tile(x1);
                     t0 += kAttnUnit;
                     if (t0 >= t_stop) break;
@@ -631,9 +738,8 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
                     work_tile(x0);
                     t0 += kAttnUnit;
                     if (t0 >= t_stop) break;
-                    pg = pn;
-                    pn = pages_of(t0 + kAttnUnit);
-                    load_tile(x0, t0, pg);
+                    if (FAST && turn == 64) place_rows(t0);
+                    load_tile(x0, t0);
                 }
             }
         }

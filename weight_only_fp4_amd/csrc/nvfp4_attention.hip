@@ -447,9 +447,10 @@ nvfp4_status nvfp4_paged_attention(const nvfp4_kv_cache* cache, const void* q, i
     while ((int64_t)2 << a.page_shift < c.shape.page_size) ++a.page_shift;
     a.page_magic = c.shape.page_size == 1 ? 0u
                    : (uint32_t)((((uint64_t)1 << (32 + a.page_shift)) + c.shape.page_size - 1) / (uint64_t)c.shape.page_size);
-    // 32-bit offsets inside a half-tile of 16 tokens
+    // 32-bit offsets: inside a half-tile of 16 tokens below 2^30, of an NVFP4 block's scales below 2^31
     const int64_t far = (int64_t)1 << 26;
-    const bool fast = c.shape.page_size % 16 == 0 && (c.format == kKvNvfp4 || (c.k.s_token < far && c.v.s_token < far));
+    const bool fast = c.shape.page_size % 16 == 0 &&
+                      (c.format == kKvNvfp4 ? c.shape.page_size < 1 << 23 : c.k.s_token < far && c.v.s_token < far);
     if (c.format == kKvE4m3) launch_attn_e4m3(a, fast, sh.workgroups, st);
     else if (c.format == kKvNvfp4) launch_attn_nvfp4(a, fast, sh.workgroups, st);
     else if (f16) launch_attn_f16(a, fast, sh.workgroups, st);
