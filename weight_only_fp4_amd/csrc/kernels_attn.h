@@ -171,11 +171,13 @@ __device__ __forceinline__ void attn_buffer_load(__amdgpu_buffer_rsrc_t r, uint3
 // key-value heads (times tiles of 16 query heads) all have that many.  The
 // units of all (sequence, head) pairs stand in one row, sequence by sequence,
 // each pair with one more place in front for what a pair costs besides its
-// tokens, and workgroup j of N takes the places from floor(j P / N) to
-// floor((j + 1) P / N) of all P, so every compute unit gets the same work
-// whatever the lengths are.  N is at most the grid, and a multiple of the pairs
-// (equal lengths are then split at equal places): with p places a pair on
-// average
+// tokens (two with an NVFP4 cache, whose units are short, where most
+// workgroups hold several pairs: 64 sequences of 1 to 8191 tokens took 45 us
+// with one, 41 with two, 42 with four), and workgroup j of N takes the places
+// from floor(j P / N) to floor((j + 1) P / N) of all P, so every compute unit
+// gets the same work whatever the lengths are.  N is at most the grid, and a
+// multiple of the pairs (equal lengths are then split at equal places): with p
+// places a pair on average
 //   p < 6      one workgroup a pair: a join costs more than four units do
 //              (2 x 300 tokens: 9.3 us, halved 10.6);
 //   p <= 17    p workgroups while no compute unit gets a second one, so each
@@ -266,6 +268,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
     };
 
     // ---- this workgroup's stretch of places [p_begin, p_end)
+    const int front = KV == kKvNvfp4 && a.B * HT > kAttnMaxWorkgroups / 2 ? 2 : 1;   // places in front of a pair's units
     int p_begin, p_end, groups = 1, b = 0;
     unsigned places = 1;
     // floor(x / y) of a 41-bit and a 31-bit number, exact in fp64: the quotient is
@@ -281,7 +284,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
             clamp_range(lengths[0], f, n);
             if (threadIdx.x == 0) {
                 s_pre[0] = 0;
-                s_pre[1] = 1 + count_units(f, n);
+                s_pre[1] = front + count_units(f, n);
             }
         } else if (w == 0) {
             int before = 0;
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
                 if (b0 + lane < a.B) {
                     int f, n;
                     clamp_range(a.lengths[b0 + lane], f, n);
-                    v = 1 + count_units(f, n);
+                    v = front + count_units(f, n);
                 }
 #pragma unroll
                 for (int d = 1; d < 64; d <<= 1) {
@@ -346,16 +349,16 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
             while (next * HT <= place) next = __builtin_amdgcn_readfirstlane(s_pre[++b + 1]);
             const int before = __builtin_amdgcn_readfirstlane(s_pre[b]);
             clamp_range(lengths[b], first, len);
-            units = next - before - 1;
+            units = next - before - front;
             const int local = place - before * HT;
-            ph = local / (units + 1);
-            pair_begin = before * HT + ph * (units + 1);
-            const int o0 = place - pair_begin;                                                 // 0: the place in front
-            const int o1 = p_end - pair_begin < units + 1 ? p_end - pair_begin : units + 1;
+            ph = local / (units + front);
+            pair_begin = before * HT + ph * (units + front);
+            const int o0 = place - pair_begin;
+            const int o1 = p_end - pair_begin < units + front ? p_end - pair_begin : units + front;
             place = pair_begin + o1;
-            unit0 = o0 > 0 ? o0 - 1 : 0;
-            unit1 = o1 - 1;
-            if (unit1 <= unit0) continue;   // only the place in front: the next workgroup begins the pair
+            unit0 = o0 > front ? o0 - front : 0;
+            unit1 = o1 - front;
+            if (unit1 <= unit0) continue;   // only places in front: the next workgroup begins the pair
         }
         const int hk = ph / a.head_tiles, ht = ph - hk * a.head_tiles;
         const int nh = a.G - ht * kAttnHeads < kAttnHeads ? a.G - ht * kAttnHeads : kAttnHeads;
@@ -824,8 +827,8 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
         // this can be the only pair that goes on past its stretch: the counter
         // is that workgroup's) to the one holding its last.
         // Workgroup j holds place p if it is the last with floor(j P / N) <= p.
-        const int j0 = quotient((int64_t)groups * (pair_begin + 2) - 1, places);
-        const int j1 = quotient((int64_t)groups * (pair_begin + units + 1) - 1, places);
+        const int j0 = quotient((int64_t)groups * (pair_begin + front + 1) - 1, places);
+        const int j1 = quotient((int64_t)groups * (pair_begin + units + front) - 1, places);
         const int parts = j1 - j0 + 1;
         if (!split_arrive(z->counters, j0, parts, &s_flag)) continue;
         // ---- the workgroup that arrived last joins all of them, in their
