@@ -28,7 +28,7 @@ inline AttnShape attn_shape(int64_t B, int64_t Hk, int64_t G, int64_t D, int64_t
     s.part_floats = (G < kAttnHeads ? G : kAttnHeads) * (D + 2);
     const int64_t units = (max_tokens + kAttnTile + kAttnUnit - 1) / kAttnUnit;
     const int64_t places = s.pairs * (units + 2);   // at most (kernels_attn.h)
-    s.split = B <= kAttnScan && places >= 8 && places < ((int64_t)1 << 31);
+    s.split = B <= kAttnScan && s.pairs * (units + 1) >= 8 && places < ((int64_t)1 << 31);
     s.workgroups = s.pairs;
     if (s.split) {
         int64_t each = units + 1;
