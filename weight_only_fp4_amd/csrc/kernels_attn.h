@@ -274,6 +274,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
     // floor(x / y) of a 41-bit and a 31-bit number, exact in fp64: the quotient is
     // further from the next integer than it is rounded by
     auto quotient = [](int64_t x, unsigned y) { return (int)((double)x / (double)y); };
+    int me = (int)blockIdx.x;   // which of the stretches
     if (!a.split) {
         b = (int)(blockIdx.x / (unsigned)HT);
         p_begin = 0;
@@ -313,9 +314,15 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
         if (each > kAttnPairSplits) each = kAttnPairSplits;
         groups = (int)(pairs * each);
         groups = groups < (int)gridDim.x ? groups : (int)gridDim.x;
-        if ((int)blockIdx.x >= groups) return;
-        p_begin = quotient((int64_t)blockIdx.x * places, groups);
-        p_end = quotient((int64_t)(blockIdx.x + 1) * places, groups);
+        if (me >= groups) return;
+        // A full grid is two workgroups a compute unit, of which the second ones
+        // start later and find the memory busy: neighbours in the row are one of
+        // either (32 x 8192 tokens: 175 us, in the grid's order 180; 8 x 4096
+        // NVFP4 17 us instead of 18.5).
+        if (groups == kAttnMaxWorkgroups)
+            me = me < kAttnMaxWorkgroups / 2 ? 2 * me : 2 * (me - kAttnMaxWorkgroups / 2) + 1;
+        p_begin = quotient((int64_t)me * places, groups);
+        p_end = quotient((int64_t)(me + 1) * places, groups);
         int lo = 0, hi = a.B;   // the sequence of the first place: the last b with HT * s_pre[b] <= p_begin
         const int at = p_begin / HT;
         while (hi - lo > 1) {
@@ -763,7 +770,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
         const int part_floats = hp * (D + 2);
         const bool whole = unit0 == 0 && unit1 == units;
         // a workgroup's partial result is its second one if the pair's first place lies inside its stretch
-        float* part = z->partials + (int64_t)(blockIdx.x * 2 + (pair_begin > p_begin ? 1 : 0)) * part_floats;
+        float* part = z->partials + (int64_t)(me * 2 + (pair_begin > p_begin ? 1 : 0)) * part_floats;
         const float vscale = KV != kKv16 && z->vc.scale ? ((AttnScales)(uint64_t)z->vc.scale)[hk] : 1.0f;
         uint16_t* out = z->out + b * z->o_b + (int64_t)head0 * z->o_h;
         float* lse = z->lse ? z->lse + (int64_t)b * z->Hq + head0 : nullptr;
