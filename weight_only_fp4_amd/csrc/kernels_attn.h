@@ -234,6 +234,15 @@ __device__ __forceinline__ void attn_buffer_load(__amdgpu_buffer_rsrc_t r, uint3
 // entry is outside the cache, get the weight 0 and their value rows are
 // replaced by zeros, so nothing in them (an infinity, a NaN) reaches the
 // result.
+//
+// What bounds it, with 8 key-value heads of 128: of 16-bit and E4M3 caches the
+// HBM reads, 32 x 8192 tokens (bf16, 1.07 GB) in 169 us and one sequence of
+// 131072 (E4M3, 268 MB) in 52, 6.3 and 5.1 TB/s with a plain read at 7.1:
+// about 10 us of a call are its beginning (the lengths, the table, the first
+// rows, one after another) and its end (the join).  Of NVFP4 caches also the
+// instructions of the decoding, 32 x 8192 tokens (302 MB) in 60 us (56 with
+// the loads alone), and where lengths differ the segments' ends, 64 sequences
+// of 1 to 8191 tokens (147 MB) in 39.  130 tokens take 7.3 us, all latency.
 template <int FMT, int DT, bool FAST>
 __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
     constexpr bool F16 = FMT != 0;                   // type of the products: 0 is a bf16 cache
