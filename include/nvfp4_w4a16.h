@@ -612,14 +612,16 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const int32_t* slots, vo
  * Products are fp32-accumulated MFMAs on bf16 (bf16 cache) or fp16 values;
  * softmax statistics and sums are fp32; results are bitwise reproducible.
  *   workspace: nvfp4_paged_attention_workspace_bytes(B, Hq, heads, D,
- *   max_pages * page_size) bytes, 256-byte aligned, zero-filled before its first
- *   use; every call leaves the counters in it zero, so one workspace serves any
+ *   max_pages * page_size) bytes, 256-byte aligned, its first
+ *   NVFP4_ATTENTION_COUNTER_BYTES zero before its first use; every call
+ *   leaves the counters in them zero, so one workspace serves any
  *   number of calls of any sizes one after another (not calls that may overlap
  *   in time, and not the GEMMs: theirs has another layout).
  * B == 0 launches nothing.  Errors: sizes, B > 65535, heads * ceil(Hq / heads / 16) >
  * 65535, Hq not a multiple of heads, max_pages < 0, max_pages * page_size >=
  * 2^30, softmax_scale not finite, window < 0, NULL pointers -> INVALID_ARG;
  * misaligned -> ALIGNMENT; workspace too small -> BUFFER_TOO_SMALL. */
+#define NVFP4_ATTENTION_COUNTER_BYTES 2048
 int64_t nvfp4_paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t heads, int64_t D, int64_t max_tokens);
 nvfp4_status nvfp4_paged_attention(const nvfp4_kv_cache* cache, const void* q, int64_t q_b, int64_t q_h,
                                    const int32_t* page_table, int64_t ld_table, int64_t max_pages,

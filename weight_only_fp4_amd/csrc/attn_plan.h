@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "../../include/nvfp4_w4a16.h"
 #include "kernels_attn.h"
 
 namespace nvfp4 {
@@ -19,6 +20,7 @@ struct AttnShape {
 // A split call's counters, one a workgroup, at the workspace's start: partial
 // results of calls of other sizes never reach them.
 constexpr int64_t kAttnCounterBytes = kAttnMaxWorkgroups * 4;
+static_assert(kAttnCounterBytes == NVFP4_ATTENTION_COUNTER_BYTES, "the header's figure");
 // Two workgroups per compute unit (the kernels take up to 256 registers a
 // lane, so eight waves fit a unit): one works while the other ends a segment.
 // Only places the lengths can give count (kernels_attn.h).

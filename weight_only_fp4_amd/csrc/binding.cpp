@@ -15,7 +15,6 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
-#include <ATen/ops/zeros.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -305,7 +304,8 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[11] == Py_None) {
         const int64_t need = nvfp4_paged_attention_workspace_bytes(B, Hq, c.heads, D, max_pages * c.page_size);
         if (need < 0) check(NVFP4_ERR_INVALID_ARG);
-        ws = at::zeros({need}, at::TensorOptions().dtype(at::kByte).device(dev));
+        ws = at::empty({need}, at::TensorOptions().dtype(at::kByte).device(dev));
+        if (need > 0) ws.narrow(0, 0, NVFP4_ATTENTION_COUNTER_BYTES).zero_();
     } else {
         ws = tensor(a[11], "workspace_buf");
         TORCH_CHECK_VALUE(ws.device() == dev && ws.is_contiguous(), "workspace_buf must be a contiguous tensor on ", dev);
