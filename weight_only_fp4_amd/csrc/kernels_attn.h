@@ -1,6 +1,8 @@
 // Attention of one new token per sequence over the paged key-value cache,
 // split over the cache's length and joined.
 #pragma once
+#include <type_traits>
+
 #include "decode.h"
 #include "kernels_gemm.h"
 #include "kernels_kv.h"
@@ -8,27 +10,31 @@
 namespace nvfp4 {
 
 struct AttnArgs {
-    const uint16_t* q;           // [B][Hq][D]
-    int64_t q_b, q_h;            // strides in elements
-    KvSide kc, vc;
+    // what a workgroup's beginning needs: one cache line
     KvShape shape;
-    const int32_t* table;        // [B][ld_table], `width` entries used
-    int64_t ld_table;
-    int width;
     const int32_t* lengths;      // [B]
     int B;
-    int G;                       // query heads per key-value head
     int head_tiles;              // ceil(G / 16)
-    int Hq;
+    int width;                   // table entries used of a sequence
     int window;                  // 0: all tokens
-    float scale_log2;            // softmax scale * log2(e)
+    int split;                   // 0: one workgroup per pair
+    int grid;                    // workgroups of a split call
+    // a segment's
     uint32_t page_magic;         // token / page_size = umulhi(token, magic) >> shift (page_size > 1)
     int page_shift;
+    const uint16_t* q;           // [B][Hq][D]
+    int64_t q_b, q_h;            // strides in elements
+    const int32_t* table;        // [B][ld_table], `width` entries used
+    int64_t ld_table;
+    KvSide kc, vc;
+    int G;                       // query heads per key-value head
+    float scale_log2;            // softmax scale * log2(e)
+    int f16;                     // q and out are fp16 (else bf16)
+    // its end's
+    int Hq;
     uint16_t* out;
     int64_t o_b, o_h;
     float* lse;                  // [B][Hq] or NULL
-    int f16;                     // q and out are fp16 (else bf16)
-    int split;                   // 0: one workgroup per pair
     float* partials;             // [workgroups][2][part_floats]: sums, then (maximum, sum of weights) pairs
     int* counters;               // [workgroups], zero between calls
 };
@@ -264,6 +270,14 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
     constexpr int PASSES = DT / kAttnOutCols, RP = 4 / PASSES;   // accumulator rows of a lane per pass
     constexpr int LD = kAttnOutCols, OS = LD + 4;                // 16-byte aligned rows, spread over the banks
 
+    // the arguments, to be read from memory again
+    typedef const __attribute__((address_space(4))) AttnArgs KernArgs;
+    auto kernel_args = [] {
+        KernArgs* z = (KernArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+        asm volatile("" : "+s"(z));
+        return z;
+    };
+
     // tokens [first, len) of sequence b; units are counted from the tile `first` lies in
     AttnTable lengths = (AttnTable)(uint64_t)a.lengths;
     const int most = a.width * ps;   // below 2^30
@@ -278,7 +292,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
 
     // ---- this workgroup's stretch of places [p_begin, p_end)
     const int front = KV == kKvNvfp4 && a.B * HT > kAttnMaxWorkgroups / 2 ? 2 : 1;   // places in front of a pair's units
-    int p_begin, p_end, groups = 1, b = 0;
+    int p_begin, p_end, groups = 1, b = 0, ph0 = 0;
     unsigned places = 1;
     // floor(x / y) of a 41-bit and a 31-bit number, exact in fp64: the quotient is
     // further from the next integer than it is rounded by
@@ -286,6 +300,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
     int me = (int)blockIdx.x;   // which of the stretches
     if (!a.split) {
         b = (int)(blockIdx.x / (unsigned)HT);
+        ph0 = (int)blockIdx.x - b * HT;
         p_begin = 0;
         p_end = 1;
     } else {
@@ -322,7 +337,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
         if (per >= kAttnWhole && per <= kAttnJoin + 1 && places <= 256) each = per;
         if (each > kAttnPairSplits) each = kAttnPairSplits;
         groups = (int)(pairs * each);
-        groups = groups < (int)gridDim.x ? groups : (int)gridDim.x;
+        groups = groups < a.grid ? groups : a.grid;
         if (me >= groups) return;
         // A full grid is two workgroups a compute unit, of which the second ones
         // start later and find the memory busy: neighbours in the row are one of
@@ -350,11 +365,15 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
     const int quarter = (p_end - p_begin + 3) / 4;
     int prio_place = p_begin + quarter, prio = 3;
     for (int place = p_begin; place < p_end;) {
+        // The arguments a segment needs are fetched when it begins: kept, they would
+        // have to make way for the loop's scalars, 60 lane writes in front of the
+        // first load (130 tokens: 7.5 us, so 7.0).
+        const KernArgs* y = kernel_args();
         // ---- the segment: units [unit0, unit1) of pair (b, ph)
         int first, len, ph, units, unit0, unit1;
         int pair_begin = 0;   // the pair's first place
         if (!a.split) {
-            ph = (int)(blockIdx.x % (unsigned)HT);
+            ph = ph0;
             clamp_range(lengths[b], first, len);
             units = count_units(first, len);
             unit0 = 0;
@@ -367,7 +386,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
             clamp_range(lengths[b], first, len);
             units = next - before - front;
             const int local = place - before * HT;
-            ph = local / (units + front);
+            ph = (int)((unsigned)local / (unsigned)(units + front));
             pair_begin = before * HT + ph * (units + front);
             const int o0 = place - pair_begin;
             const int o1 = p_end - pair_begin < units + front ? p_end - pair_begin : units + front;
@@ -376,16 +395,16 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
             unit1 = o1 - front;
             if (unit1 <= unit0) continue;   // only places in front: the next workgroup begins the pair
         }
-        const int hk = ph / a.head_tiles, ht = ph - hk * a.head_tiles;
-        const int nh = a.G - ht * kAttnHeads < kAttnHeads ? a.G - ht * kAttnHeads : kAttnHeads;
-        const int head0 = hk * a.G + ht * kAttnHeads;
+        const int hk = y->head_tiles == 1 ? ph : (int)((unsigned)ph / (unsigned)y->head_tiles), ht = ph - hk * y->head_tiles;
+        const int nh = y->G - ht * kAttnHeads < kAttnHeads ? y->G - ht * kAttnHeads : kAttnHeads;
+        const int head0 = hk * y->G + ht * kAttnHeads;
         const int base_t = first & ~(kAttnTile - 1);
         const int t_stop = len - base_t < unit1 * kAttnUnit ? len : base_t + unit1 * kAttnUnit;
 
         // q of head c as the B operand of each 32-column step: the columns of
         // step j are the ones the key pieces deliver
         uint4 qf[KSTEPS];
-        float qk_log2 = a.scale_log2;
+        float qk_log2 = y->scale_log2;
         auto key_column = [&](int j) {   // first of the 8 columns lane (g, c) holds in step j
             if constexpr (KV == kKv16) return j * 32 + g * 8;
             else if constexpr (KV == kKvE4m3) return (j >> 1) * 64 + g * 16 + (j & 1) * 8;
@@ -393,17 +412,16 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
             else return (j >> 2) * 128 + g * 32 + (j & 3) * 8;
         };
         {
-            const uint16_t* qr = a.q + b * a.q_b + (int64_t)(head0 + (c < nh ? c : 0)) * a.q_h;
+            const uint16_t* qr = y->q + b * y->q_b + (int64_t)(head0 + (c < nh ? c : 0)) * y->q_h;
 #pragma unroll
             for (int j = 0; j < KSTEPS; ++j) {
                 const int col = key_column(j);
-                const bool in = c < nh && (FAST || col < D);
-                qf[j] = in ? *reinterpret_cast<const uint4*>(qr + col) : make_uint4(0u, 0u, 0u, 0u);
+                qf[j] = c < nh && (FAST || col < D) ? *reinterpret_cast<const uint4*>(qr + col) : make_uint4(0u, 0u, 0u, 0u);
             }
         }
 
-        const uint64_t kb = (uint64_t)a.kc.base + hk * a.kc.s_head, vb = (uint64_t)a.vc.base + hk * a.vc.s_head;
-        auto page_index = [&](int t) { return ps == 1 ? t : (int)(__umulhi((uint32_t)t, a.page_magic) >> a.page_shift); };
+        const uint64_t kb = (uint64_t)y->kc.base + hk * y->kc.s_head, vb = (uint64_t)y->vc.base + hk * y->vc.s_head;
+        auto page_index = [&](int t) { return !FAST && ps == 1 ? t : (int)(__umulhi((uint32_t)t, y->page_magic) >> y->page_shift); };
         auto in_cache = [&](int p) { return (uint32_t)p < (uint32_t)a.shape.pages; };
 
         constexpr int KP = KV == kKv16 ? KSTEPS : KV == kKvE4m3 ? KSTEPS / 2 : (DT == 256 ? 2 : 1);   // pieces of a key row
@@ -414,10 +432,11 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
             uint32_t kraw[2][KP][4], ksc[2][KP], vraw[8][VW], vsc[8];
             uint32_t valid;
         };
-        const int64_t scales_at = (int64_t)ps * (D / 2);   // NVFP4: from a block's start to its scales
+        // NVFP4: from a block's start to its scales (below 2^31 where it is FAST)
+        const std::conditional_t<FAST, uint32_t, int64_t> scales_at = (std::conditional_t<FAST, uint32_t, int64_t>)ps * (D / 2);
         // FAST: the lane's offsets inside a half-tile
-        const uint32_t k_tok = KV == kKvNvfp4 ? (uint32_t)(D / 2) : (uint32_t)a.kc.s_token;
-        const uint32_t v_tok = KV == kKvNvfp4 ? (uint32_t)(D / 2) : (uint32_t)a.vc.s_token;
+        const uint32_t k_tok = KV == kKvNvfp4 ? (uint32_t)(D / 2) : (uint32_t)y->kc.s_token;
+        const uint32_t v_tok = KV == kKvNvfp4 ? (uint32_t)(D / 2) : (uint32_t)y->vc.s_token;
         // WIDE: of an NVFP4 value row a lane loads the quarter c / 4 of token 4 g +
         // c % 4, and four lanes then exchange pieces so that each has its columns
         // of the four tokens: 8 loads a tile instead of 20 with the lane's own
@@ -449,15 +468,18 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
         auto fetch_entries = [&](int t) {
             const int mine = lane_token(t);
             ahead = -1;
-            if (mine < t_stop) ahead = a.table[b * a.ld_table + page_index(mine)];
+            const KernArgs* y = kernel_args();
+            if (mine < t_stop) ahead = y->table[b * y->ld_table + page_index(mine)];
         };
         auto place_rows = [&](int t) {   // of the 32 tiles from the one at t
+            const KernArgs* y = kernel_args();
             const int mine = lane_token(t);
             const bool ok = in_cache(ahead);
-            const int64_t page = ok ? ahead : 0, tok = ok ? mine - page_index(mine) * ps : 0;
-            at_k = (uint32_t)((page * a.kc.s_page + tok * k_tok) >> 4);
-            at_v = (uint32_t)((page * a.vc.s_page + tok * v_tok) >> 4);
-            if constexpr (KV == kKvNvfp4) deep = (uint32_t)(scales_at - tok * (D / 2 - D / 16));
+            // offsets in 16 bytes fit 32 bits, and so do the strides where there is more than one page
+            const uint32_t page = ok ? (uint32_t)ahead : 0u, tok = ok ? (uint32_t)(mine - page_index(mine) * ps) : 0u;
+            at_k = page * (uint32_t)(y->kc.s_page >> 4) + tok * (k_tok >> 4);
+            at_v = page * (uint32_t)(y->vc.s_page >> 4) + tok * (v_tok >> 4);
+            if constexpr (KV == kKvNvfp4) deep = scales_at - tok * (uint32_t)(D / 2 - D / 16);
             out_of_cache = __ballot(!ok);
             odd = __ballot(!ok || mine < first || mine + 16 > t_stop);
             turn = 0;
@@ -561,7 +583,10 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
         f32x4 acc[VD];
 #pragma unroll
         for (int e = 0; e < VD; ++e) acc[e] = f32x4{0.f, 0.f, 0.f, 0.f};
-        float m = -INFINITY, l = 0.f;
+        // columns without a head have q = 0 and, by this maximum, the weights 0 (with a
+        // copy of the first head in them 64 ragged NVFP4 sequences took 41 us instead
+        // of 39.7: it seems the power of the products, not their number)
+        float m = c < nh ? -INFINITY : INFINITY, l = 0.f;
 
         auto work_tile = [&](Tile& x) {
             // ---- scores
@@ -594,13 +619,16 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) s[i] = sc[i >> 2][i & 3] * qk_log2;
             if (x.valid != 0xFFFFFFFFu) {
-                asm volatile("");   // a branch: as selects the masks cost every tile 50 operations
+                // a branch: as selects the masks cost every tile 50 operations, and worked
+                // out ahead their bits cost every workgroup's beginning
+                int gm = g;
+                asm volatile("" : "+v"(gm));
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const bool ok = (x.valid >> ((i >> 2) * 16 + g * 4 + (i & 3))) & 1u;
+                    const bool ok = (x.valid >> ((i >> 2) * 16 + gm * 4 + (i & 3))) & 1u;
                     s[i] = ok ? s[i] : -INFINITY;
                     // the value row loaded into x.vraw[i]
-                    const bool row_ok = WIDE ? (x.valid >> ((i >> 2) * 16 + g * 4 + (c & 3))) & 1u : ok;
+                    const bool row_ok = WIDE ? (x.valid >> ((i >> 2) * 16 + gm * 4 + (c & 3))) & 1u : ok;
                     if constexpr (KV == kKvNvfp4) {
                         if (!WIDE || (i & 3) == 0) x.vsc[i] = row_ok ? x.vsc[i] : 0u;
                     }
@@ -714,7 +742,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
                 float f[KSTEPS][8];
 #pragma unroll
                 for (int j = 0; j < KSTEPS; ++j) {
-                    if (a.f16) unpack8<true>(qf[j], f[j]);
+                    if (y->f16) unpack8<true>(qf[j], f[j]);
                     else unpack8<false>(qf[j], f[j]);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -736,7 +764,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
                     qf[j] = pack8<true>(f[j]);
                 }
                 qk_log2 *= __uint_as_float((uint32_t)ex << 23);
-                if (a.kc.scale) qk_log2 *= ((AttnScales)(uint64_t)a.kc.scale)[hk];
+                if (y->kc.scale) qk_log2 *= ((AttnScales)(uint64_t)y->kc.scale)[hk];
             }
             if constexpr (AHEAD) {
                 for (;;) {
@@ -766,9 +794,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
         // ---- join the waves: every lane's sum is of its own tokens, its
         // maximum of all four groups'.  The arguments this part needs are
         // fetched again, so that the loop does not have to keep them.
-        const __attribute__((address_space(4))) AttnArgs* z =
-            (const __attribute__((address_space(4))) AttnArgs*)__builtin_amdgcn_kernarg_segment_ptr();
-        asm volatile("" : "+s"(z));
+        const KernArgs* z = kernel_args();
         l += __shfl_xor(l, 16);
         l += __shfl_xor(l, 32);
         if (g == 0) {

@@ -438,6 +438,7 @@ nvfp4_status nvfp4_paged_attention(const nvfp4_kv_cache* cache, const void* q, i
     a.lse = lse;
     a.f16 = f16 != 0;
     a.split = sh.split;
+    a.grid = (int)sh.workgroups;
     a.B = (int)B;
     a.counters = static_cast<int*>(workspace);
     a.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAttnCounterBytes);
