@@ -13,7 +13,7 @@ namespace {
 template <int DT, bool FAST>
 void launch(const AttnArgs& a, int64_t workgroups, hipStream_t st) {
     const int nh = a.G < kAttnHeads ? a.G : kAttnHeads;
-    const size_t out = (size_t)kAttnWaves * nh * (kAttnOutCols + 4) * sizeof(float);
+    const size_t out = (size_t)kAttnWaves * nh * ((DT < kAttnOutCols ? DT : kAttnOutCols) + 4) * sizeof(float);
     const size_t join = (size_t)kAttnMaxWorkgroups * nh * sizeof(float);   // factors of every partial result
     hipLaunchKernelGGL((k_paged_attn<NVFP4_KV_FMT, DT, FAST>), dim3((unsigned)workgroups), dim3(kAttnThreads),
                        out > join ? out : join, st, a);

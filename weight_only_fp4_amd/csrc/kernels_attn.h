@@ -50,7 +50,8 @@ constexpr int kAttnPairSplits = 64;                         // at most this many
                                                             // last of them joins what they leave
 constexpr unsigned kAttnWhole = 6;                          // pairs of fewer places are not split
 constexpr int kAttnJoin = 16;                               // partial results a join fetches at a time
-constexpr int kAttnOutCols = 64;                            // columns of the accumulators that go through LDS at a time
+constexpr int kAttnOutCols = 128;                           // columns of the accumulators that go through LDS at a time (at most):
+                                                            // 64 at a time take 0.2 us more a segment (D = 128)
 
 // Read-only memory at a uniform address (scalar loads), and rows of the cache.
 typedef const __attribute__((address_space(4))) int32_t* AttnTable;
@@ -267,8 +268,8 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
     __shared__ int s_flag;
     // the waves' accumulators on their way out: [waves][nh][OS], a pass at a time
     extern __shared__ float s_o[];
-    constexpr int PASSES = DT / kAttnOutCols, RP = 4 / PASSES;   // accumulator rows of a lane per pass
-    constexpr int LD = kAttnOutCols, OS = LD + 4;                // 16-byte aligned rows, spread over the banks
+    constexpr int LD = DT < kAttnOutCols ? DT : kAttnOutCols, OS = LD + 4;   // 16-byte aligned rows, spread over the banks
+    constexpr int PASSES = DT / LD, RP = 4 / PASSES;                         // accumulator rows of a lane per pass
 
     // the arguments, to be read from memory again
     typedef const __attribute__((address_space(4))) AttnArgs KernArgs;
@@ -401,6 +402,20 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
         const int base_t = first & ~(kAttnTile - 1);
         const int t_stop = len - base_t < unit1 * kAttnUnit ? len : base_t + unit1 * kAttnUnit;
 
+        // The wave's table entries come first: its rows wait for them.  FAST: of the
+        // half-tiles of 32 tiles, else of a tile's tokens.
+        int t0 = base_t + unit0 * kAttnUnit + w * kAttnTile;
+        auto page_index = [&](int t) { return !FAST && ps == 1 ? t : (int)(__umulhi((uint32_t)t, y->page_magic) >> y->page_shift); };
+        int ahead = -1;   // the lane's table entry
+        auto lane_token = [&](int t) { return FAST ? t + (lane >> 1) * kAttnUnit + (lane & 1) * 16 : t + lane; };
+        auto fetch_entries = [&](int t) {
+            const int mine = lane_token(t);
+            ahead = -1;
+            const KernArgs* y = kernel_args();
+            if (mine < t_stop && (FAST || lane < kAttnTile)) ahead = y->table[b * y->ld_table + page_index(mine)];
+        };
+        fetch_entries(t0);
+
         // q of head c as the B operand of each 32-column step: the columns of
         // step j are the ones the key pieces deliver
         uint4 qf[KSTEPS];
@@ -412,16 +427,19 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
             else return (j >> 2) * 128 + g * 32 + (j & 3) * 8;
         };
         {
-            const uint16_t* qr = y->q + b * y->q_b + (int64_t)(head0 + (c < nh ? c : 0)) * y->q_h;
+            const uint16_t* qr = y->q + b * y->q_b + (int64_t)(head0 + c) * y->q_h;
 #pragma unroll
-            for (int j = 0; j < KSTEPS; ++j) {
-                const int col = key_column(j);
-                qf[j] = c < nh && (FAST || col < D) ? *reinterpret_cast<const uint4*>(qr + col) : make_uint4(0u, 0u, 0u, 0u);
+            for (int j = 0; j < KSTEPS; ++j) qf[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (c < nh) {
+#pragma unroll
+                for (int j = 0; j < KSTEPS; ++j) {
+                    const int col = key_column(j);
+                    if (FAST || col < D) qf[j] = *reinterpret_cast<const uint4*>(qr + col);
+                }
             }
         }
 
         const uint64_t kb = (uint64_t)y->kc.base + hk * y->kc.s_head, vb = (uint64_t)y->vc.base + hk * y->vc.s_head;
-        auto page_index = [&](int t) { return !FAST && ps == 1 ? t : (int)(__umulhi((uint32_t)t, y->page_magic) >> y->page_shift); };
         auto in_cache = [&](int p) { return (uint32_t)p < (uint32_t)a.shape.pages; };
 
         constexpr int KP = KV == kKv16 ? KSTEPS : KV == kKvE4m3 ? KSTEPS / 2 : (DT == 256 ? 2 : 1);   // pieces of a key row
@@ -462,15 +480,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
         // instead of two table lookups and their 64-bit products.
         uint32_t at_k = 0, at_v = 0, deep = 0;
         uint64_t odd = 0, out_of_cache = 0;   // half-tiles that are not whole; whose entry is outside the cache
-        int ahead = -1;                       // the lane's table entry of the 32 tiles after those
         int turn = 0;                         // lane of the next tile
-        auto lane_token = [&](int t) { return t + (lane >> 1) * kAttnUnit + (lane & 1) * 16; };
-        auto fetch_entries = [&](int t) {
-            const int mine = lane_token(t);
-            ahead = -1;
-            const KernArgs* y = kernel_args();
-            if (mine < t_stop) ahead = y->table[b * y->ld_table + page_index(mine)];
-        };
         auto place_rows = [&](int t) {   // of the 32 tiles from the one at t
             const KernArgs* y = kernel_args();
             const int mine = lane_token(t);
@@ -532,7 +542,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
                 const int page = ahead, tok = t + lane - page_index(t + lane) * ps;
                 const bool ok = in_cache(page);
                 x.valid = token_mask(t) & (uint32_t)__ballot(ok);
-                ahead = lane < kAttnTile && t + kAttnUnit + lane < t_stop ? a.table[b * a.ld_table + page_index(t + kAttnUnit + lane)] : -1;
+                fetch_entries(t + kAttnUnit);
                 if (lane < kAttnTile) {
                     // offsets in units of 16 bytes; a masked row is the head's first in its place
                     s_off[w][0][lane] = ok ? (uint32_t)((page * a.kc.s_page + (KV == kKvNvfp4 ? 0 : tok * a.kc.s_token)) >> 4) : 0u;
@@ -726,15 +736,9 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
         // ---- the tiles.  Loads run one tile ahead where the registers hold
         // two tiles (with the accumulators and q within 200 of 256).  Two ahead
         // are slower: 131072 tokens (E4M3) 63 us instead of 56.
-        int t0 = base_t + unit0 * kAttnUnit + w * kAttnTile;
         constexpr bool AHEAD = FAST && 2 * (KP * 8 + VW * 8) + VD * 4 + KSTEPS * 4 <= 200;
         if (t0 < t_stop) {
-            if constexpr (FAST) {
-                fetch_entries(t0);
-                place_rows(t0);
-            } else if (lane < kAttnTile && t0 + lane < t_stop) {
-                ahead = a.table[b * a.ld_table + page_index(t0 + lane)];
-            }
+            if constexpr (FAST) place_rows(t0);
             Tile x0, x1;
             load_tile(x0, t0);
             if constexpr (KV != kKv16) {   // q to fp16, while the first tile is on its way
