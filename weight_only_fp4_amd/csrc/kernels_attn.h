@@ -179,18 +179,18 @@ __device__ __forceinline__ void attn_buffer_load(__amdgpu_buffer_rsrc_t r, uint3
 // units of all (sequence, head) pairs stand in one row, sequence by sequence,
 // each pair with one more place in front for what a pair costs besides its
 // tokens (two with an NVFP4 cache, whose units are short, where most
-// workgroups hold several pairs: 64 sequences of 1 to 8191 tokens took 45 us
-// with one, 41 with two, 42 with four), and workgroup j of N takes the places
+// workgroups hold several pairs: 64 sequences of up to 8191 tokens take 42.5
+// us with one, 40 with two or four), and workgroup j of N takes the places
 // from floor(j P / N) to floor((j + 1) P / N) of all P, so every compute unit
 // gets the same work whatever the lengths are.  N is at most the grid, and a
 // multiple of the pairs (equal lengths are then split at equal places): with p
 // places a pair on average
 //   p < 6      one workgroup a pair: a join costs more than four units do
-//              (2 x 300 tokens: 9.3 us, halved 10.6);
+//              (2 x 300 tokens: 8.3 us, halved 9.4);
 //   p <= 17    p workgroups while no compute unit gets a second one, so each
 //              works on one unit and the join takes one round trip (1 x 1024
-//              tokens: 9.4 us, p / 2 workgroups 11.4, p / 4 13.5);
-//   else       p / 2 (1 x 8192 tokens: 15.9 us, p / 4 17.3, p 19.7: the join
+//              tokens: 8.4 us, p / 2 workgroups 10.4, p / 4 12.5);
+//   else       p / 2 (1 x 8192 tokens: 14.8 us, p / 4 16.3, p 17.2: the join
 //              of more than 16 partial results takes several).
 // A stretch is a few segments, each a run of units of one pair; a segment that
 // is not the whole pair leaves a partial result, and the workgroup that arrives
@@ -244,12 +244,12 @@ __device__ __forceinline__ void attn_buffer_load(__amdgpu_buffer_rsrc_t r, uint3
 //
 // What bounds it, with 8 key-value heads of 128: of 16-bit and E4M3 caches the
 // HBM reads, 32 x 8192 tokens (bf16, 1.07 GB) in 169 us and one sequence of
-// 131072 (E4M3, 268 MB) in 52, 6.3 and 5.1 TB/s with a plain read at 7.1:
-// about 10 us of a call are its beginning (the lengths, the table, the first
+// 131072 (E4M3, 268 MB) in 51, 6.4 and 5.2 TB/s with a plain read at 7.1:
+// about 9 us of a call are its beginning (the lengths, the table, the first
 // rows, one after another) and its end (the join).  Of NVFP4 caches also the
 // instructions of the decoding, 32 x 8192 tokens (302 MB) in 60 us (56 with
 // the loads alone), and where lengths differ the segments' ends, 64 sequences
-// of 1 to 8191 tokens (147 MB) in 39.  130 tokens take 7.3 us, all latency.
+// of up to 8191 tokens (147 MB) in 37.  130 tokens take 6.5 us, all latency.
 template <int FMT, int DT, bool FAST>
 __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
     constexpr bool F16 = FMT != 0;                   // type of the products: 0 is a bf16 cache
@@ -342,8 +342,8 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
         if (me >= groups) return;
         // A full grid is two workgroups a compute unit, of which the second ones
         // start later and find the memory busy: neighbours in the row are one of
-        // either (32 x 8192 tokens: 175 us, in the grid's order 180; 8 x 4096
-        // NVFP4 17 us instead of 18.5).
+        // either (32 x 8192 tokens: 175 us, in the grid's order 181; 8 x 4096
+        // NVFP4 16 us instead of 17.5).
         if (groups == kAttnMaxWorkgroups)
             me = me < kAttnMaxWorkgroups / 2 ? 2 * me : 2 * (me - kAttnMaxWorkgroups / 2) + 1;
         p_begin = quotient((int64_t)me * places, groups);
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
         // WIDE: of an NVFP4 value row a lane loads the quarter c / 4 of token 4 g +
         // c % 4, and four lanes then exchange pieces so that each has its columns
         // of the four tokens: 8 loads a tile instead of 20 with the lane's own
-        // columns, which cost more than the exchange (32 x 8192 tokens: 67 -> 62
+        // columns, which cost more than the exchange (32 x 8192 tokens: 65 -> 60
         // us).  A row of 64 columns has only two bytes a lane to exchange.
         constexpr bool WIDE = FAST && KV == kKvNvfp4 && DT >= 128;
         const uint32_t k_lane = c * k_tok + g * KB;
