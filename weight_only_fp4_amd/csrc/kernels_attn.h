@@ -103,6 +103,17 @@ __device__ __forceinline__ float attn_wave_reduce(float v, Op op) {
     return op(v, __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x121, 0xF, 0xF, true)));
 }
 
+// Sums over the lanes up to each: within rows of 16 by 1, 2, 4 and 8 lanes,
+// then rows 0 and 2 onto the next, then the first two rows onto the others.
+__device__ __forceinline__ int attn_wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr:1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast:15
+    return v + __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // row_bcast:31
+}
+
 // Lane i of four gets the j-th's x[i] as x[j]: the square of four lanes and
 // four registers, transposed.
 __device__ __forceinline__ void attn_quad_transpose(uint32_t& x0, uint32_t& x1, uint32_t& x2, uint32_t& x3, int lane) {
@@ -313,21 +324,18 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
                 s_pre[1] = front + count_units(f, n);
             }
         } else if (w == 0) {
-            int before = 0;
+            int before = 0, ahead = lane < a.B ? a.lengths[lane] : 0;
             for (int b0 = 0; b0 < a.B; b0 += 64) {
                 int v = 0;
                 if (b0 + lane < a.B) {
                     int f, n;
-                    clamp_range(a.lengths[b0 + lane], f, n);
+                    clamp_range(ahead, f, n);
                     v = front + count_units(f, n);
                 }
-#pragma unroll
-                for (int d = 1; d < 64; d <<= 1) {
-                    const int t = __shfl_up(v, d);
-                    if (lane >= d) v += t;
-                }
+                ahead = b0 + 64 + lane < a.B ? a.lengths[b0 + 64 + lane] : 0;
+                v = attn_wave_scan(v);
                 if (b0 + lane < a.B) s_pre[b0 + lane + 1] = before + v;
-                before += __shfl(v, 63);
+                before += __builtin_amdgcn_readlane(v, 63);
             }
             if (lane == 0) s_pre[0] = 0;
         }
