@@ -609,8 +609,9 @@ nvfp4_status nvfp4_kv_read(const nvfp4_kv_cache* cache, const int32_t* slots, vo
  *   q [B][Hq][D] and out [B][Hq][D] of the activation type (strides q_b, q_h,
  *   o_b, o_h; out may be q with the same strides), lse fp32 [B][Hq] or NULL, page_table int32
  *   [B][ld_table] (max_pages entries used), lengths int32 [B].
- * Products are fp32-accumulated MFMAs on bf16 (bf16 cache) or fp16 values;
- * softmax statistics and sums are fp32; results are bitwise reproducible.
+ * Products are fp32-accumulated MFMAs on bf16 (bf16 cache) or fp16 values, in
+ * which a weight w_t has 16 (bf16), 22 (fp16, E4M3 cache) or 11 bits (NVFP4
+ * cache); softmax statistics and sums are fp32; results are bitwise reproducible.
  *   workspace: nvfp4_paged_attention_workspace_bytes(B, Hq, heads, D,
  *   max_pages * page_size) bytes, 256-byte aligned, its first
  *   NVFP4_ATTENTION_COUNTER_BYTES zero before its first use; every call

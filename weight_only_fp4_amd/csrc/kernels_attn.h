@@ -243,10 +243,18 @@ __device__ __forceinline__ void attn_buffer_load(__amdgpu_buffer_rsrc_t r, uint3
 //
 // Quantised caches are decoded to fp16, which holds E4M3 and E2M1 x E4M3
 // exactly; q is scaled to [1, 2) by a power of two per head so that it fits,
-// and the weights p <= 1 are rounded to fp16 (bf16 with a bf16 cache) for the
-// second product; the sum of the weights is taken in fp32 before that.  The
-// heads' key scale goes into the softmax scale, the value scale into the
-// final normalisation.
+// and the weights p <= 1 go into the second product as fp16 (bf16 with a bf16
+// cache); the sum of the weights is taken in fp32 before that.  With a 16-bit
+// or E4M3 cache they go as two values, the rounded weight and what the
+// rounding took off, with a product each: 16 bits of a weight with bf16, 22
+// with fp16 (rounded once they added a sixth to the error of a 16-bit result).
+// These kernels wait for memory, so the second product costs them nothing (32
+// x 8192 tokens bf16: 174.9 us with and without, in a graph; 131072 E4M3 54.1
+// and 54.0; 1000 short sequences, E4M3, 89 and 87.4).  With an NVFP4 cache it
+// would (32 x 8192: 61 -> 64 us, 64 ragged ones 38.5 -> 40.8), for bits that a
+// value of four has no use for: there a weight is one fp16, off by 2^-11 of
+// itself.  The heads' key scale goes into the softmax scale, the value scale
+// into the final normalisation.
 //
 // Tokens past the length or before the window, and tokens of pages whose table
 // entry is outside the cache, get the weight 0 and their value rows are
@@ -267,6 +275,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
     constexpr int KV = FMT <= 1 ? kKv16 : FMT == 2 ? kKvE4m3 : kKvNvfp4;
     constexpr int KSTEPS = DT / 32;                  // 32-column steps of the first product
     constexpr int VD = DT / 16;                      // value columns of a lane
+    constexpr bool FINE = KV != kKvNvfp4;            // weights in two parts
     const int D = FAST ? DT : a.shape.D;
     const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -675,6 +684,14 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
             }
             const uint4 pf = make_uint4(pack_round2<F16>(p[0], p[1]), pack_round2<F16>(p[2], p[3]),
                                         pack_round2<F16>(p[4], p[5]), pack_round2<F16>(p[6], p[7]));
+            uint4 pl = pf;   // FINE: what that rounding took off them
+            if constexpr (FINE) {
+                const uint32_t d[4] = {pf.x, pf.y, pf.z, pf.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) p[i] -= act_to_f32<F16>((i & 1) ? d[i >> 1] >> 16 : d[i >> 1] & 0xFFFFu);
+                pl = make_uint4(pack_round2<F16>(p[0], p[1]), pack_round2<F16>(p[2], p[3]),
+                                pack_round2<F16>(p[4], p[5]), pack_round2<F16>(p[6], p[7]));
+            }
             uint32_t vs[4];   // NVFP4: group scales of the token pairs
             if constexpr (KV == kKvNvfp4) {
 #pragma unroll
@@ -728,8 +745,11 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < EN; ++e)
-                    acc[e0 + e] = mma16<F16>(make_uint4(vt[0][e], vt[1][e], vt[2][e], vt[3][e]), pf, acc[e0 + e]);
+                for (int e = 0; e < EN; ++e) {
+                    const uint4 vf = make_uint4(vt[0][e], vt[1][e], vt[2][e], vt[3][e]);
+                    acc[e0 + e] = mma16<F16>(vf, pf, acc[e0 + e]);
+                    if constexpr (FINE) acc[e0 + e] = mma16<F16>(vf, pl, acc[e0 + e]);
+                }
             }
         };
 
