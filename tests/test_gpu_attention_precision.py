@@ -63,3 +63,50 @@ def test_weights_keep_more_bits_than_the_type_of_the_products(kind, dt):
     assert np.median(np.abs(want) / size) > 4 * rel            # the rounding of the weights would show
     assert np.all(np.abs(out[:, 0] - want) <= off + (np.abs(want) + off) * ref.u(dt) + ref.least(dt))
     assert np.all(np.abs(lse[:, 0] - np.log(total[:, 0])) <= 2.0 ** -20)
+
+
+@pytest.mark.parametrize("kind,dt", [("same", BF), ("same", HF), ("fp8", BF), ("fp8", HF), ("fp4", BF), ("fp4", HF)])
+def test_many_small_weights_add_up(kind, dt):
+    """One token of 32 is far above the others, which each weigh e^-18 of it (below fp16's least value), and the others'
+    values make the result.  A weight is off by the exponential's 2^-20 of itself, the score's four roundings and its
+    own, and with products in fp16 by half its least value on a scale of 2^7."""
+    say(f"small weights {kind} {dt}")
+    D, n = 64, 4096
+    q = torch.zeros((1, 1, D), dtype=torch.float64)
+    k, v = torch.zeros((1, n, 1, D), dtype=torch.float64), torch.full((1, n, 1, D), 6.0, dtype=torch.float64)
+    q[..., 0] = 1
+    k[..., 0] = -18
+    k[:, ::32], v[:, ::32] = 0, 0
+    out, lse, kk, vv = attend(q, k, v, kind, dt)
+    assert np.all(kk[0, 1:32, 0, 0] == -18) and np.all(vv[0, 1:32] == 6)
+    w = 31 * np.exp(-18.0)
+    want = 6 * w / (1 + w)
+    u = 2.0 ** -8 if kind == "same" and dt == BF else 2.0 ** -11
+    off = want * (u + 2.0 ** -20 + 4 * 18 * ref.U32 + 2 * (n + 64) * ref.U32) + 6 * 31 * 2.0 ** -32
+    assert np.all(np.abs(out - want) <= off + (want + off) * ref.u(dt) + ref.least(dt))
+    assert np.all(np.abs(lse - np.log(n // 32) - np.log1p(w)) <= 2 * (n + 64) * ref.U32 + 2.0 ** -20)
+
+
+@pytest.mark.parametrize("kind,dt", [("same", BF), ("same", HF), ("fp8", BF), ("fp8", HF), ("fp4", BF), ("fp4", HF)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_of_every_size(kind, dt, sign):
+    """Four equal scores from 2^-6 to 2^60, whose last place passes everything the running maximum is kept apart by, and
+    a fifth below them by a quarter: the mean of four, or of five where the fifth is near."""
+    D, n = 64, 5
+    size = 2.0 ** torch.arange(-6, 61)[:, None]
+    k, v = torch.zeros((1, n, 1, D), dtype=torch.float64), torch.zeros((1, n, 1, D), dtype=torch.float64)
+    k[..., 0] = sign * 4.0
+    k[:, 4, :, 0] = 3.0 if sign > 0 else -6.0
+    v[:] = torch.tensor([1.0, 2.0, 3.0, 6.0, 1.5]).double()[None, :, None, None]
+    q = torch.zeros((1, 1, D), dtype=torch.float64)
+    q[..., 0] = 1
+    for scale in size.flatten().tolist():
+        say(f"scale {scale} {kind} {dt}")
+        out, lse, kk, vv = attend(q, k, v, kind, dt, scale=scale)
+        s = scale * kk[0, :, 0, 0]
+        w = np.exp(s - s.max())
+        want = (w[:, None] * vv[0, :, 0]).sum(0) / w.sum()
+        # the fifth score is off by four roundings of itself, which is what its weight is off by
+        rel = 2.0 ** -8 + min(1.0, np.expm1(min(8 * ref.U32 * np.abs(s).max(), 1.0))) * w[4] * 2
+        assert np.all(np.abs(out[0, 0] - want) <= np.abs(want) * (rel + 2 * ref.u(dt)) + ref.least(dt))
+        assert np.all(np.abs(lse - (s.max() + np.log(w.sum()))) <= 8 * ref.U32 * np.abs(s).max() + 2.0 ** -20)

@@ -243,8 +243,15 @@ __device__ __forceinline__ void attn_buffer_load(__amdgpu_buffer_rsrc_t r, uint3
 //
 // Quantised caches are decoded to fp16, which holds E4M3 and E2M1 x E4M3
 // exactly; q is scaled to [1, 2) by a power of two per head so that it fits,
-// and the weights p <= 1 go into the second product as fp16 (bf16 with a bf16
-// cache); the sum of the weights is taken in fp32 before that.  With a 16-bit
+// and the weights go into the second product as fp16 (bf16 with a bf16 cache);
+// the sum of the weights is taken in fp32 before that.  The running maximum m
+// is kept 7 below the largest score (in powers of two) where the product is of
+// fp16, so the weights are at most 2^7, or 2^8 where a score's last place is
+// above 1 and 7 is rounded, and those down to 2^-32 of the largest are not
+// rounded to 0: what vanishes adds up to less than a rounding of fp16 for up to
+// 2^21 tokens of a wave (2^14 with 1 as the largest weight, where a tile's 31
+// tokens of 2^-26 beside one of zero values gave 0).  8 could be rounded to 16,
+// at a last place of 16, and overflow.  With a 16-bit
 // or E4M3 cache they go as two values, the rounded weight and what the
 // rounding took off, with a product each: 16 bits of a weight with bf16, 22
 // with fp16 (rounded once they added a sixth to the error of a 16-bit result).
@@ -276,6 +283,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
     constexpr int KSTEPS = DT / 32;                  // 32-column steps of the first product
     constexpr int VD = DT / 16;                      // value columns of a lane
     constexpr bool FINE = KV != kKvNvfp4;            // weights in two parts
+    constexpr float ABOVE = F16 ? 7.0f : 0.0f;       // log2 of the largest weight
     const int D = FAST ? DT : a.shape.D;
     const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -666,7 +674,7 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
             float top = s[0];
 #pragma unroll
             for (int i = 1; i < 8; ++i) top = fmaxf(top, s[i]);
-            top = attn_head_max(top);
+            top = attn_head_max(top) - ABOVE;
             if (__any(top > m)) {
                 const float mn = fmaxf(m, top);
                 const float down = m == mn ? 1.0f : __builtin_amdgcn_exp2f(m - mn);   // m = -inf gives 0
