@@ -110,3 +110,32 @@ def test_scores_of_every_size(kind, dt, sign):
         rel = 2.0 ** -8 + min(1.0, np.expm1(min(8 * ref.U32 * np.abs(s).max(), 1.0))) * w[4] * 2
         assert np.all(np.abs(out[0, 0] - want) <= np.abs(want) * (rel + 2 * ref.u(dt)) + ref.least(dt))
         assert np.all(np.abs(lse - (s.max() + np.log(w.sum()))) <= 8 * ref.U32 * np.abs(s).max() + 2.0 ** -20)
+
+
+@pytest.mark.parametrize("kind", ["fp8", "fp4"])
+@pytest.mark.parametrize("dt,far,size", [(BF, 2.0 ** 26, 1.0), (HF, 2.0 ** 15, 2.0 ** -8)])
+def test_columns_far_below_the_largest_of_a_query_count(kind, dt, far, size):
+    """Queries whose largest column meets keys of zero: the scores are made of columns 2^-23 to 2^-26 of it.  With a
+    quantised cache a column is held as fp16 on a scale where the largest is 2^14 or more, so it is off by 2^-39 of
+    that; the rest as in attention_ref.attention."""
+    say(f"far columns {kind} {dt}")
+    g = torch.Generator()
+    g.manual_seed(7)
+    D, n, G = 128, 200, 3
+    q, k, v = (torch.randn(s, generator=g).to(dt).double() for s in ((1, G, D), (1, n, 1, D), (1, n, 1, D)))
+    q = (q * size).to(dt).double()
+    q[..., 5] = far
+    k[..., 5] = 0
+    scale = 0.125 / size
+    out, lse, kk, vv = attend(q, k, v, kind, dt, scale=scale)
+    q, kk, vv = q[0].numpy(), kk[0, :, 0], vv[0, :, 0]
+    want, want_lse, _, _ = ref.attention(q, kk, vv, scale, (HF, dt))
+    s = q @ kk.T * scale
+    ds = (np.abs(q) @ np.abs(kk).T * scale * (D + 6) * ref.U32 + np.abs(s) * 2 * ref.U32
+          + 2.0 ** -39 * far * np.abs(kk).sum(1)[None] * scale).max(1, keepdims=True)
+    w = np.exp(s - s.max(1, keepdims=True))
+    each = w @ np.abs(vv) / w.sum(1, keepdims=True)
+    off = each * (ref.u(HF) + np.expm1(4 * ds) + 2.0 ** -20 + 2 * (n + 64) * ref.U32) + 2.0 ** -32 * np.abs(vv).sum(0)
+    assert np.all(off < 0.02 * np.abs(vv).max())
+    assert np.all(np.abs(out[0] - want) <= off + (np.abs(want) + off) * ref.u(dt) + ref.least(dt))
+    assert np.all(np.abs(lse[0] - want_lse) <= 2 * ds[:, 0] + (n + 64) * ref.U32 + 2.0 ** -20)

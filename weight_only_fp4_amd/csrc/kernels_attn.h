@@ -242,8 +242,11 @@ __device__ __forceinline__ void attn_buffer_load(__amdgpu_buffer_rsrc_t r, uint3
 //          (each wave its own, no barrier).
 //
 // Quantised caches are decoded to fp16, which holds E4M3 and E2M1 x E4M3
-// exactly; q is scaled to [1, 2) by a power of two per head so that it fits,
-// and the weights go into the second product as fp16 (bf16 with a bf16 cache);
+// exactly; q is scaled by a power of two per head, its largest column to [2^14,
+// 2^15), so that it fits: only columns below 2^-28 of that one (2^-31 with a
+// bf16 q) lose bits.
+//
+// The weights go into the second product as fp16 (bf16 with a bf16 cache);
 // the sum of the weights is taken in fp32 before that.  The running maximum m
 // is kept 7 below the largest score (in powers of two) where the product is of
 // fp16, so the weights are at most 2^7, or 2^8 where a score's last place is
@@ -794,16 +797,17 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
                 top = o > top ? o : top;
                 o = __shfl_xor(top, 32);
                 top = o > top ? o : top;
+                // the largest to [2^14, 2^15): 2^14 more than [1, 2) for the columns below it
                 int ex = (int)(top >> 23);
-                ex = ex < 1 ? 1 : (ex > 253 ? 253 : ex);
-                const float down = __uint_as_float((uint32_t)(254 - ex) << 23);   // 2^(127 - ex)
+                ex = ex < 15 ? 15 : (ex > 253 ? 253 : ex);
+                const float down = __uint_as_float((uint32_t)(268 - ex) << 23);   // 2^(141 - ex)
 #pragma unroll
                 for (int j = 0; j < KSTEPS; ++j) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) f[j][e] *= down;
                     qf[j] = pack8<true>(f[j]);
                 }
-                qk_log2 *= __uint_as_float((uint32_t)ex << 23);
+                qk_log2 *= __uint_as_float((uint32_t)(ex - 14) << 23);
                 if (y->kc.scale) qk_log2 *= ((AttnScales)(uint64_t)y->kc.scale)[hk];
             }
             if constexpr (AHEAD) {
