@@ -505,7 +505,7 @@ nvfp4_status nvfp4_moe_fc1_f16(const void* x, int64_t ld_x, int64_t T, const int
  *   for scales); rows and leading dimensions of 16 bytes (8 for 8-bit y) and N
  *   a multiple of 8 up to 32768 take the one-pass kernel.
  * T == 0 launches nothing.  Errors: T < 0, T rows that take 2^32 threads or
- * more (from T = 2^22 on), N < 1 or N >= 2^31, a leading dimension < N, eps
+ * more (from T = 2^22 on), N < 1 or N > 2^31 - 256, a leading dimension < N, eps
  * negative or not finite, h without residual, NULL x / weight / y ->
  * INVALID_ARG; misaligned -> ALIGNMENT. */
 nvfp4_status nvfp4_rms_norm(const void* x, int64_t ld_x, const void* residual, int64_t ld_r, const void* weight,

@@ -183,10 +183,11 @@ __global__ void __launch_bounds__(64 * kNormMaxWaves) k_rms_norm(NormArgs a) {
     }
 }
 
-// Any row length, stride and alignment: one workgroup of 256 threads per row,
-// single values, the row read again for each of the two or three passes.
-// With h the later passes read h back (each thread its own values), so h may
-// be the residual's or x's own memory; y is written in the last pass only.
+// Any row length up to 2^31 - 256 (the 32-bit counters then end below 2^31),
+// stride and alignment: one workgroup of 256 threads per row, single values,
+// the row read again for each of the two or three passes.  With h the later
+// passes read h back (each thread its own values), so h may be the residual's
+// or x's own memory; y is written in the last pass only.
 template <bool F16, bool F8>
 __global__ void __launch_bounds__(256) k_rms_norm_any(NormArgs a) {
     __shared__ float s_sum[4];

@@ -203,7 +203,8 @@ nvfp4_status nvfp4_rms_norm(const void* x, int64_t ld_x, const void* residual, i
                             int64_t N, int f16, void* stream) {
     const char* fn = "nvfp4_rms_norm";
     const int64_t lim = (int64_t)1 << 31;
-    if (T < 0 || T >= lim || N < 1 || N >= lim)
+    // the column counters are 32 bits wide and go on 256 past the last column
+    if (T < 0 || T >= lim || N < 1 || N > lim - 256)
         return fail(NVFP4_ERR_INVALID_ARG, "%s: T = %lld, N = %lld", fn, (long long)T, (long long)N);
     if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(NVFP4_ERR_INVALID_ARG, "%s: eps must be finite and not negative", fn);
     if (h && !residual) return fail(NVFP4_ERR_INVALID_ARG, "%s: h is only written with a residual", fn);
