@@ -32,6 +32,17 @@ __device__ __forceinline__ bool kv_locate(const KvShape& s, int32_t slot, int64_
     return page < s.pages;
 }
 
+// Codes and group scales of token `tok` in an NVFP4 block, which may pass 2 GB
+// (a page of 2^24 tokens of 256 columns): 64-bit offsets.
+template <typename B>
+__device__ __forceinline__ B* kv_code_row(B* block, const KvShape& s, int tok) {
+    return block + (int64_t)tok * (s.D / 2);
+}
+template <typename B>
+__device__ __forceinline__ B* kv_scale_row(B* block, const KvShape& s, int tok) {
+    return block + (int64_t)s.page_size * (s.D / 2) + (int64_t)tok * (s.D / 16);
+}
+
 // ------------------------------------------------------------------ rotary --
 
 struct RopeArgs {
@@ -145,8 +156,8 @@ __device__ __forceinline__ void kv_store16(const KvSide& side, const KvShape& sh
         if (!there) return;
         const uint32_t b0 = nvfp4_group_scale(__uint_as_float(m0), r), b1 = nvfp4_group_scale(__uint_as_float(m1), r);
         const float f0 = nvfp4_group_factor(b0, r), f1 = nvfp4_group_factor(b1, r);
-        uint8_t* row = block + tok * (sh.D / 2);
-        uint8_t* srow = block + (int64_t)sh.page_size * (sh.D / 2) + tok * (sh.D / 16);
+        uint8_t* row = kv_code_row(block, sh, tok);
+        uint8_t* srow = kv_scale_row(block, sh, tok);
         *reinterpret_cast<uint32_t*>(row + c0 / 2) = nvfp4_codes8(lo, f0);
         *reinterpret_cast<uint32_t*>(row + c1 / 2) = nvfp4_codes8(hi, f1);
         if (!pair || (c0 & 8) == 0) srow[c0 / 16] = (uint8_t)b0;
@@ -286,8 +297,8 @@ __device__ __forceinline__ void kv_load16(const KvSide& side, const KvShape& sh,
             f[(i & 1) * 4 + 3] = q.y;
         }
     } else {
-        const uint2 b = *reinterpret_cast<const uint2*>(block + tok * (sh.D / 2) + c0 / 2);
-        const float s = e4m3_to_f32(block[(int64_t)sh.page_size * (sh.D / 2) + tok * (sh.D / 16) + c0 / 16]);
+        const uint2 b = *reinterpret_cast<const uint2*>(kv_code_row(block, sh, tok) + c0 / 2);
+        const float s = e4m3_to_f32(kv_scale_row(block, sh, tok)[c0 / 16]);
 #define NVFP4_KV_PAIR(WORD, BYTE, F, I)                                                 \
     {                                                                                   \
         const f32x2 p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(WORD, 1.0f, BYTE);     \
