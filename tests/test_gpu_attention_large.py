@@ -6,7 +6,7 @@ import torch
 
 import attention_ref as ref
 import weight_only_fp4_amd as nv
-from test_gpu_attention import BF, DEV, HF, gen, normal, say
+from test_gpu_attention import BF, DEV, HF, Paged, gen, normal, say
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +42,28 @@ def test_nvfp4_blocks_past_two_gigabytes(D, page):
                                   torch.tensor([page], dtype=torch.int32, device=DEV), window=40, return_lse=True)
     o, l, bo, bl = ref.attention(ref.f64(q[0]), held[0][-40:, 0], held[1][-40:, 0], ref.default_scale(D), (HF, BF))
     assert np.all(np.abs(ref.f64(out[0]) - o) <= bo) and np.all(np.abs(ref.f64(lse[0]) - l) <= bl)
+
+
+@pytest.mark.parametrize("kind", ["same", "fp8", "fp4"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [3968, 4095, 4096, 4097, 4224, 8192, 8300])
+def test_segments_of_more_tiles_than_are_looked_up_at_once(n, D, kind):
+    """More sequences than are counted: each is one segment, whose waves look their pages up 32 tiles (4096 tokens) at a
+    time.  One and two lookups, filled and begun; a window that starts inside the first; pages outside the cache behind
+    it."""
+    say(f"segment of {n} tokens, D={D}, {kind}")
+    lengths = [0] * 2049
+    lengths[1027] = n
+    p = Paged(lengths, 3, 1, D, 16, kind, BF if D != 128 else HF, seed=n)
+    p.check(p.run())
+    for window in (n - 75, 4097):
+        if window < n:
+            p.check(p.run(window=window), window=window)
+    table = p.table.clone()
+    out = [70, 253, 254, 257, 300, 513]
+    for page in out:
+        if page < table.shape[1]:
+            table[1027, page] = -1 if page % 2 else p.kc.shape[0]
+    keep = [np.ones(m, dtype=bool) for m in lengths]
+    keep[1027] = ~np.isin(np.arange(n) // 16, out)
+    p.check(p.run(table=table), keep=keep)

@@ -521,7 +521,9 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
             out_of_cache = __ballot(!ok);
             odd = __ballot(!ok || mine < first || mine + 16 > t_stop);
             turn = 0;
+            // past the segment's end there are none: such tiles are outside the cache
             if (t + 32 * kAttnUnit < t_stop) fetch_entries(t + 32 * kAttnUnit);
+            else ahead = -1;
         };
         auto load_tile = [&](Tile& x, int t) {
             if constexpr (FAST) {
