@@ -489,7 +489,7 @@ nvfp4_status nvfp4_moe_fc1_f16(const void* x, int64_t ld_x, int64_t T, const int
  * and the attention over it.  f16 selects fp16 activations (0: bf16); every
  * 16-bit array of a call has that type.  Strides are in elements of the array
  * unless a byte stride is named.  All rows start 16-byte aligned and are
- * contiguous, except where stated. */
+ * contiguous, except where stated.  Rows that are written share no memory. */
 
 /* Root-mean-square norm.  Row t of T, N values:
  *   h = residual ? RNE16(x + residual) : x          (stored to h if given)

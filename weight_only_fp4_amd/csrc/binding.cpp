@@ -13,6 +13,7 @@
 // Nvfp4Error.
 #include <Python.h>
 
+#include <ATen/MemoryOverlap.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
@@ -73,9 +74,17 @@ at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, c10::Device dev) {
     return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
 }
 
+// What is written to: rows that share memory (an expanded tensor's) would be written by several workgroups at once.
+void own_rows(const at::Tensor& t, const char* name) {
+    TORCH_CHECK_VALUE(at::has_internal_overlap(t) != at::MemOverlap::Yes, name, " is written to: its rows must not share memory");
+}
+
 // `o` as the output of that shape, or a new one if it is None.
 at::Tensor output(PyObject* o, const char* name, at::ScalarType type, at::IntArrayRef shape, c10::Device dev) {
-    return o == Py_None ? fresh(shape, type, dev) : same(o, name, type, shape, dev);
+    if (o == Py_None) return fresh(shape, type, dev);
+    const at::Tensor& t = same(o, name, type, shape, dev);
+    own_rows(t, name);
+    return t;
 }
 
 void* stream_of(c10::Device dev) { return c10::hip::getCurrentHIPStream(dev.index()).stream(); }
@@ -234,6 +243,8 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     c10::DeviceGuard guard(dev);
     const int64_t T = k.size(0);
     const nvfp4_kv_cache c = cache_of(a[7], a[8], a[10], a[11], type, dev);
+    own_rows(tensor(a[7], "k_cache"), "k_cache");
+    own_rows(tensor(a[8], "v_cache"), "v_cache");
     same(a[1], "k", type, {T, c.heads, c.head_dim}, dev);
     const at::Tensor& v = same(a[2], "v", type, {T, c.heads, c.head_dim}, dev);
     const at::Tensor& slots = same(a[9], "slots", at::kInt, {T}, dev);
