@@ -581,7 +581,9 @@ nvfp4_status nvfp4_rope_apply(const nvfp4_rope* rope, const void* x, int64_t x_t
 /* Appends T tokens to the cache: keys k [T][heads][D] (strides k_t, k_h) and
  * values v go to row slots[t] % page_size of page slots[t] / page_size; tokens
  * whose slot is negative or past the cache are skipped (padding).  Two tokens
- * with one slot leave either one's row.  With rope the keys are rotated first
+ * with one slot leave a row made of pieces of both (16 columns at a time are
+ * written together, and an NVFP4 group's scale apart from its codes): a call's
+ * slots are distinct.  With rope the keys are rotated first
  * and rounded to 16 bits (R a multiple of 32 for NVFP4_KV_NVFP4, at most 256),
  * and queries q [T][Hq][D] are rotated into q_out in the same launch, padding
  * included (q_out may be q; Hq = 0 and NULL without queries).

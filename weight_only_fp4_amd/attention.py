@@ -85,8 +85,8 @@ def kv_cache(pages, heads, page_size, head_dim, dtype, device="cuda"):
 
 def kv_write(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None):
     """Quantises (by the caches' dtype) and writes k, v [T, heads, D] to rows slots int32 [T] of the cache, row s of the
-    cache being token s % page_size of page s // page_size; tokens with a negative slot are skipped.  k_scale, v_scale:
-    fp32 [heads], the values' scales in an 8- or 4-bit cache (None: 1)."""
+    cache being token s % page_size of page s // page_size; tokens with a negative slot are skipped, the others' slots
+    distinct.  k_scale, v_scale: fp32 [heads], the values' scales in an 8- or 4-bit cache (None: 1)."""
     (_binding or _native()).kv_append(None, k, v, None, None, None, False, k_cache, v_cache, slots, k_scale, v_scale,
                                       None)
 
