@@ -127,6 +127,7 @@ def paged_attention(q, k_cache, v_cache, page_table, lengths, scale=None, k_scal
     sequence b in page page_table[b, t // page_size] (int32 [B, max_pages]), lengths int32 [B] tokens (0: the output is
     0).  scale defaults to 1 / sqrt(D); window > 0: the last ``window`` tokens only.  Returns out [B, Hq, D], or (out,
     lse fp32 [B, Hq]).  workspace_buf: ``workspace(paged_attention_workspace_bytes(...), device)``, reusable by calls
-    of any sizes on one stream; made per call if not given."""
+    of any sizes on one stream; made per call if not given.  Batches of more than 2048 sequences are not split over their
+    lengths: very long ones are better called for in smaller batches."""
     return (_binding or _native()).paged_attention(q, k_cache, v_cache, page_table, lengths, scale, k_scale, v_scale,
                                                    window, out, return_lse, workspace_buf)

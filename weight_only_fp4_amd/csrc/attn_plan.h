@@ -24,6 +24,11 @@ static_assert(kAttnCounterBytes == NVFP4_ATTENTION_COUNTER_BYTES, "the header's 
 // Two workgroups per compute unit (the kernels take up to 256 registers a
 // lane, so eight waves fit a unit): one works while the other ends a segment.
 // Only places the lengths can give count (kernels_attn.h).
+// More than kAttnScan sequences are not split: their unit counts would not fit
+// LDS, and such batches fill the chip with a workgroup per pair (2048 of 40
+// tokens and one of 8192, 8 heads of 128, bf16: 152 us; 2047 and it, split, 249).
+// Only one sequence far longer than all others then takes longer (131072: 1716
+// us and 328).
 inline AttnShape attn_shape(int64_t B, int64_t Hk, int64_t G, int64_t D, int64_t max_tokens) {
     AttnShape s;
     s.pairs = B * Hk * ((G + kAttnHeads - 1) / kAttnHeads);
