@@ -189,9 +189,10 @@ __device__ __forceinline__ void attn_buffer_load(__amdgpu_buffer_rsrc_t r, uint3
 // key-value heads (times tiles of 16 query heads) all have that many.  The
 // units of all (sequence, head) pairs stand in one row, sequence by sequence,
 // each pair with one more place in front for what a pair costs besides its
-// tokens (two with an NVFP4 cache, whose units are short, where most
-// workgroups hold several pairs: 64 sequences of up to 8191 tokens take 42.5
-// us with one, 40 with two or four), and workgroup j of N takes the places
+// tokens (two with an NVFP4 cache, whose units take less time, and more pairs
+// than half the grid, where a workgroup that takes short sequences holds several
+// pairs: 64 sequences of up to 8191 tokens, 512 pairs, 42.5 us with one, 40 with
+// two or four), and workgroup j of N takes the places
 // from floor(j P / N) to floor((j + 1) P / N) of all P, so every compute unit
 // gets the same work whatever the lengths are.  N is at most the grid, and a
 // multiple of the pairs (equal lengths are then split at equal places): with p
@@ -273,12 +274,16 @@ __device__ __forceinline__ void attn_buffer_load(__amdgpu_buffer_rsrc_t r, uint3
 //
 // What bounds it, with 8 key-value heads of 128: of 16-bit and E4M3 caches the
 // HBM reads, 32 x 8192 tokens (bf16, 1.07 GB) in 169 us and one sequence of
-// 131072 (E4M3, 268 MB) in 51, 6.4 and 5.2 TB/s with a plain read at 7.1:
-// about 9 us of a call are its beginning (the lengths, the table, the first
-// rows, one after another) and its end (the join).  Of NVFP4 caches also the
-// instructions of the decoding, 32 x 8192 tokens (302 MB) in 60 us (56 with
-// the loads alone), and where lengths differ the segments' ends, 64 sequences
-// of up to 8191 tokens (147 MB) in 37.  130 tokens take 6.5 us, all latency.
+// 131072 (E4M3, 268 MB) in 51 (kernel trace), 6.4 and 5.2 TB/s with a plain read
+// at 7.1: about 9 us of a call are its beginning (the lengths, the table, the
+// first rows, one after another) and its end (the join).  NVFP4 caches take 32 x
+// 8192 tokens (302 MB) in 54 us and 64 sequences of up to 8191 (147 MB) in 37.7.
+// In a graph with other calls those take 60 and 39, one of 131072 35.7, and with
+// the work on the tiles left out 54, 33 and 33.9: most of the distance to the
+// read rate is in the loads themselves (few bytes under way: a tile is 4.6 KB,
+// in 16 bits 16) and in the beginnings and ends of the segments, of which the
+// ragged ones have more; the decoding adds 5 to 18 %.  130 tokens take 6.7 us,
+// all latency.
 template <int FMT, int DT, bool FAST>
 __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
     constexpr bool F16 = FMT != 0;                   // type of the products: 0 is a bf16 cache
@@ -775,8 +780,9 @@ __global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
         };
 
         // ---- the tiles.  Loads run one tile ahead where the registers hold
-        // two tiles (with the accumulators and q within 200 of 256).  Two ahead
-        // are slower: 131072 tokens (E4M3) 63 us instead of 56.
+        // two tiles (with the accumulators and q within 200 of 256; the scales
+        // and transposes, not counted here, take NVFP4 at D = 256 to 262).  Two
+        // ahead are slower: 131072 tokens (E4M3) 63 us instead of 56.
         constexpr bool AHEAD = FAST && 2 * (KP * 8 + VW * 8) + VD * 4 + KSTEPS * 4 <= 200;
         if (t0 < t_stop) {
             if constexpr (FAST) place_rows(t0);

@@ -179,8 +179,10 @@ constexpr int kRopeUnitWords = 20;
 // pass.  All of a unit's loads come before its stores and no two units share
 // a column, so q_out may be q.
 // Bound by HBM (the reads and writes of q, k and v): 4096 tokens of 32 + 8
-// heads of 128 into an E4M3 cache (93 MB) take 19.8 us, 4.7 TB/s, a large
-// copy's rate; q alone, 5003 tokens of 16 heads of 80 (26 MB), 7.1 us; 16
+// heads of 128 into an E4M3 cache (92 MB) take 20.7 us, 4.5 TB/s (a large copy
+// reaches 4.8), into an NVFP4 cache (89 MB) 20.2; q alone, 5003 tokens of 16
+// heads of 80 (26 MB), 7.6 us; 1003 tokens of 24 + 24 heads of 64 (18.5 MB) 7.5,
+// where each token is a workgroup and its 288 units a second round of 32; 16
 // tokens 3.3 .. 4.4 us, of which the fp64 angles and the loads after the
 // barrier are most.  16 values a thread keeps every 16-bit access 16 bytes
 // wide and a whole NVFP4 group within two lanes.
@@ -313,7 +315,8 @@ __device__ __forceinline__ void kv_load16(const KvSide& side, const KvShape& sh,
 
 // Thread: 16 columns of one row; RNE16(value * head scale), zeros for a slot
 // outside the cache.  Bound by the bytes it moves: 4096 tokens of 8 heads of
-// 128 from E4M3 (25 MB, most of it just written) take 7.5 us, 16 tokens 2.5.
+// 128 from E4M3 (25 MB, most of it just written) take 7.3 us, from NVFP4 7.7, 16
+// tokens 2.9: with so few bytes a thread the divisions of its index count too.
 template <int FMT, bool F16>
 __global__ void __launch_bounds__(256) k_kv_read(ReadArgs a) {
     const int U = a.shape.D >> 4, per_token = 2 * a.shape.heads * U;

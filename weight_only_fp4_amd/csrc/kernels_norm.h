@@ -106,9 +106,10 @@ __global__ void __launch_bounds__(256) k_rms_norm_short(NormArgs a) {
 
 // One workgroup per row, the row held in registers (V 16-byte pieces a
 // thread): one pass over HBM, which bounds it from some hundred rows on: 8192
-// rows of 5120 with a residual (336 MB) take 54 .. 57 us, 5.9 .. 6.2 TB/s, and
-// 777 rows to E4M3 (28 MB) 8.2.  One row of 4096 takes 2.0 us: a load, the
-// sum over the waves and a store one after another.  N, the leading
+// rows of 5120 with a residual (336 MB) take 55 us, 6.1 TB/s, and 777 rows to
+// E4M3 (28 MB) 8.7 (calls in a graph).  One row of 4096 takes the kernel 2.0 us,
+// a call of it in a graph 3.2: a load, the sum over the waves and a store one
+// after another.  N, the leading
 // dimensions and the pointers keep 16-byte alignment (checked on the host).
 template <bool F16, bool F8, int V, bool PAST>
 __global__ void __launch_bounds__(64 * kNormMaxWaves) k_rms_norm(NormArgs a) {

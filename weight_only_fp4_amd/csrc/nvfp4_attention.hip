@@ -35,8 +35,9 @@ void launch_norm(const NormArgs& a, bool vec, hipStream_t st) {
         return;
     }
     // Rows of up to 256 values (heads): 16 or 32 lanes a row, several rows a
-    // workgroup (60000 x 128: 17.1 us with a wave each, 11.4 so; from 512 values
-    // on a wave each is faster, 20000 x 512 13.2 us against 14.2).
+    // workgroup (60000 x 128: 18.3 us with a wave each, 11.6 so; from 512 values
+    // on a wave each is faster, 20000 x 512 13.1 us against 14.2).  Figures here
+    // are of calls in a graph.
     const int pieces = a.N / 8;
     if (pieces <= 16) {
         hipLaunchKernelGGL((k_rms_norm_short<F16, F8, 16>), dim3((unsigned)((a.T + 15) / 16)), dim3(256), 0, st, a);
@@ -47,12 +48,12 @@ void launch_norm(const NormArgs& a, bool vec, hipStream_t st) {
         return;
     }
     // Longer ones: a workgroup a row, one piece a thread while the rows leave
-    // compute units free (a row's latency counts: 1 x 4096 3.5 us against 3.9
-    // with two pieces), two from there on (half the waves to start for the
-    // same loads in flight: 8192 x 5120 to 8 bits 59 -> 49 us), four where a
-    // row needs them.  Calls that move more than the 256 MB Infinity Cache
-    // holds read past it (8192 x 5120, 16 bits: 60 -> 54 us; 2048 x 4096, whose
-    // 67 MB it does hold, would lose 25 %).
+    // compute units free (a row's latency counts: 1 x 4096 3.2 us against 3.5
+    // with two pieces, 64 x 2048 2.9 and 3.1), two from there on (half the waves
+    // to start for the same loads in flight: 777 x 5120 to 8 bits 9.5 -> 8.7 us,
+    // 8192 x 5120 62 -> 50), four where a row needs them.  Calls that move more
+    // than the 256 MB Infinity Cache holds read past it (8192 x 5120, 16 bits:
+    // 60 -> 55 us; 2048 x 4096, whose 67 MB it does hold, would take 14.5 for 11.4).
     const int V = pieces > 2048 ? 4 : (pieces > 1024 || a.T >= 256 ? 2 : 1);
     const int threads = ((pieces + V - 1) / V + 63) / 64 * 64;
     const bool past = a.T * a.N * (2 + (a.r ? 2 : 0) + (a.h ? 2 : 0) + (F8 ? 1 : 2)) > (int64_t)256 << 20;
