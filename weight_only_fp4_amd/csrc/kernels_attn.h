@@ -284,8 +284,12 @@ __device__ __forceinline__ void attn_buffer_load(__amdgpu_buffer_rsrc_t r, uint3
 // in 16 bits 16) and in the beginnings and ends of the segments, of which the
 // ragged ones have more; the decoding adds 5 to 18 %.  130 tokens take 6.7 us,
 // all latency.
+//
+// With heads of 64 the registers stay within 168, so that three workgroups fit a
+// compute unit: calls of more than 2048 sequences, which are not split, have that
+// many (3000 of up to 500 tokens, 8 heads, bf16: 207 us, with two of them 245).
 template <int FMT, int DT, bool FAST>
-__global__ void __launch_bounds__(kAttnThreads) k_paged_attn(AttnArgs a) {
+__global__ void __launch_bounds__(kAttnThreads, DT == 64 ? 3 : 0) k_paged_attn(AttnArgs a) {
     constexpr bool F16 = FMT != 0;                   // type of the products: 0 is a bf16 cache
     constexpr int KV = FMT <= 1 ? kKv16 : FMT == 2 ? kKvE4m3 : kKvNvfp4;
     constexpr int KSTEPS = DT / 32;                  // 32-column steps of the first product
