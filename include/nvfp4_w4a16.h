@@ -637,6 +637,124 @@ nvfp4_status nvfp4_paged_attention(const nvfp4_kv_cache* cache, const void* q, i
                                    void* out, int64_t o_b, int64_t o_h, float* lse, void* workspace,
                                    int64_t workspace_bytes, int f16, void* stream);
 
+/* ---- Around the layers of a decode step ----------------------------------------
+ *
+ * What a step runs before, beside and after the operators above: page tables
+ * and slots from the requests' lengths, low-rank adapters beside a shared
+ * projection, the expert layer of a few tokens in one call, and the next token
+ * from its logits.  Alignment, strides, f16 and asynchrony as above. */
+
+/* Page tables, slots and positions of a step's new tokens.  Request b of B has
+ * cached[b] tokens in the cache and brings fresh[b] more; its pages of
+ * page_size tokens are page_table[b][0 .. ceil(cached[b] / page_size)).  The
+ * step's T rows hold the requests' new tokens one request after another:
+ *   offsets[b] = min(T, sum_{a<b} max(0, fresh[a])),  b in [0, B],
+ *   row offsets[b] + i is token cached[b] + i of request b:
+ *     requests[row] = b, positions[row] = cached[b] + i,
+ *     slots[row] = page_table[b][position / page_size] * page_size + position % page_size,
+ * and requests take the pages that they need further from free_pages [F],
+ * from place head[0] on, in their order; those are entered into page_table.
+ *   lengths[b] = cached[b] + fresh[b],  head_out[0] = head[0] + the pages taken.
+ * A request is refused, which leaves its row of page_table as it was, when a
+ * length is negative, its pages do not fit the max_pages entries of a row, its
+ * rows do not fit T, or its pages and those of the requests before it (refused
+ * for this reason among them) do not fit the list: lengths[b] is then
+ * max(0, cached[b]).  Rows of refused requests and rows behind the last one
+ * have slot -1, position 0, request -1.  An entry or page outside [0, 2^31 /
+ * page_size) gives slot -1.  Pages in the list are not checked for being used.
+ *   Every array is int32 on the device: cached, fresh, lengths [B], page_table
+ *   [B][ld_table], offsets [B + 1], head, head_out [1], slots, positions,
+ *   requests [T].  lengths may be cached's memory and head_out head's, so that a
+ *   captured step advances by itself; no other overlap.
+ *   workspace: nvfp4_kv_plan_workspace_bytes(B, T) bytes (0 for small calls), 8-byte
+ *   aligned, any contents.
+ * Errors: sizes (B, T, max_pages * page_size < 2^30, F < 2^31, ld_table), NULL
+ * pointers -> INVALID_ARG; misaligned -> ALIGNMENT; workspace too small ->
+ * BUFFER_TOO_SMALL. */
+int64_t nvfp4_kv_plan_workspace_bytes(int64_t B, int64_t T); /* < 0 if invalid */
+nvfp4_status nvfp4_kv_plan(const int32_t* cached, const int32_t* fresh, int64_t B, int32_t* page_table, int64_t ld_table,
+                           int64_t max_pages, int64_t page_size, const int32_t* free_pages, int64_t F, const int32_t* head,
+                           int64_t T, int32_t* slots, int32_t* positions, int32_t* requests, int32_t* lengths,
+                           int32_t* offsets, int32_t* head_out, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Low-rank adapters beside a shared projection: with a = adapter[t],
+ *   out[t] = RNE16(y[t] + scale[a] * (x[t] A_a^T) B_a^T),
+ * or y[t] unchanged where a is outside [0, L).  Sums are fp32; x A_a^T enters
+ * the second product with 16 (bf16) or 22 (fp16) bits.
+ *   x [T][ld_x] of K values, y and out [T][ld_y], [T][ld_o] of N (out may be y
+ *   with the same leading dimension; no other overlap), a [L] matrices [R][K]
+ *   (strides a_l, a_r), b [L] matrices [N][R] (strides b_l, b_n), adapter int32
+ *   [T], scale fp32 [L] or NULL for 1.  Rows of x, a and b are 16-byte aligned;
+ *   y and out need 2 bytes (16-byte aligned rows are faster).
+ *   workspace: nvfp4_lora_workspace_bytes(T, K, N, R) bytes, 16-byte aligned,
+ *   any contents.
+ * R a multiple of 8 in [8, 128], K a multiple of 8.  T == 0 or N == 0 launches
+ * nothing.  Errors: sizes (T <= 1048560, K and N < 2^24), NULL pointers ->
+ * INVALID_ARG; misaligned -> ALIGNMENT; workspace too small -> BUFFER_TOO_SMALL. */
+int64_t nvfp4_lora_workspace_bytes(int64_t T, int64_t K, int64_t N, int64_t R); /* < 0 if invalid */
+nvfp4_status nvfp4_lora_add(const void* x, int64_t ld_x, const void* a, int64_t a_l, int64_t a_r, const void* b, int64_t b_l,
+                            int64_t b_n, const int32_t* adapter, const float* scale, const void* y, int64_t ld_y, void* out,
+                            int64_t ld_o, int64_t T, int64_t K, int64_t N, int64_t R, int64_t L, void* workspace,
+                            int64_t workspace_bytes, int f16, void* stream);
+
+/* A whole mixture-of-experts layer for a few tokens, T <= 64 and T * k <= 512:
+ *   h = g1[e] * (X'[t] W1_e^T),  a = RNE16(silu(h_gate) * h_up) or RNE16(max(h, 0)^2),
+ *   out[t] = RNE16(sum_j topk_weights[t][j] * g2[e] * (a' W2_e^T)),  e = topk_ids[t][j],
+ * X' and a' with the pre-quant scales applied (pre_scale1 [H], pre_scale2 [I];
+ * RNE16) where given.  Unlike the separate calls (nvfp4_moe_fc1, the grouped
+ * GEMM, nvfp4_moe_combine), which round h and the experts' outputs to 16 bits,
+ * only a is rounded on the way; sums are fp32 and bitwise reproducible.  A pair
+ * whose id is outside [0, E) adds nothing; a token may name an expert twice.
+ *   x [T][ld_x] of H values, topk_ids int32 and topk_weights fp32 [T][k], w_fc1 a
+ *   blob of nvfp4_repack_gated (NVFP4_MOE_SILU_GLU) or nvfp4_repack
+ *   (NVFP4_MOE_RELU2) of E experts, I and H; w_fc2 of nvfp4_repack (E, H, I);
+ *   global scales fp32 [E], or NULL with mx (blobs of mxfp4_repack_gated /
+ *   mxfp4_repack); out [T][ld_o] of H values, not x.
+ *   workspace: nvfp4_moe_layer_workspace_bytes(T, k, E, H, I) bytes, 256-byte
+ *   aligned, its first NVFP4_MOE_LAYER_COUNTER_BYTES zero before its first use;
+ *   every call leaves them zero, so one workspace serves any number of these
+ *   calls of any sizes one after another (not calls that may overlap in time,
+ *   and no other operator's).
+ * T == 0 launches nothing.  Errors: sizes (H and I multiples of 16, with mx of
+ * 32, below 2^22), activation, mx, NULL pointers, global scales with mx ->
+ * INVALID_ARG; misaligned -> ALIGNMENT; workspace too small -> BUFFER_TOO_SMALL. */
+#define NVFP4_MOE_LAYER_COUNTER_BYTES 4096
+int64_t nvfp4_moe_layer_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I); /* < 0 if invalid */
+nvfp4_status nvfp4_moe_layer(const void* x, int64_t ld_x, const int32_t* topk_ids, const float* topk_weights, int64_t T,
+                             int64_t k, const void* pre_scale1, const void* w_fc1, const float* global_scales1,
+                             const void* pre_scale2, const void* w_fc2, const float* global_scales2,
+                             int global_scale_is_divisor, int activation, void* out, int64_t ld_o, int64_t E, int64_t H,
+                             int64_t I, void* workspace, int64_t workspace_bytes, int f16, int mx, void* stream);
+
+/* The next token of each row from its logits l [B][ld] of V values (type: one
+ * of NVFP4_LOGITS_*; NaN counts as -infinity).  With m the row's largest
+ * logit, t = temperature[b] and w_i = exp((l_i - m) / t), tokens ordered by (l
+ * descending, i ascending), these are kept:
+ *   the first top_k[b] (all if top_k[b] < 1);
+ *   of those, the ones before which the sum of w is < top_p[b] times the sum of
+ *   w of those, the first always (all if top_p[b] >= 1 or NaN);
+ *   of those, the ones with w >= min_p[b], the largest always.
+ * tokens[b] is the kept token, in the order of i, at which the cumulative sum of
+ * w first exceeds u[b] times its total (u in [0, 1); below it, or NaN, counts as
+ * 0, above it as the last), and logprobs[b] = ln(w / total).  t <= 0 or NaN: the
+ * first largest, logprob 0.  A row of -infinities: token -1, logprob -infinity.
+ * A largest logit of +infinity leaves only those that equal it.
+ * The weights are computed in fp64 and rounded to multiples of 2^-s, s = min(52,
+ * 62 - ceil(log2 V)): sums are exact and results do not depend on timing.
+ *   u fp32 [B]; temperature (NULL: 1), top_p, min_p fp32 [B], top_k int32 [B]
+ *   (NULL: off); tokens int32 [B]; logprobs fp32 [B] or NULL.  Rows of logits
+ *   need only their type's alignment, and may share memory (ld below V).
+ *   workspace: nvfp4_sample_workspace_bytes(B, V) bytes, 256-byte aligned, any
+ *   contents.
+ * B == 0 launches nothing.  Errors: sizes (B < 2^22, V in [1, 2^23], ld < 0),
+ * NULL pointers -> INVALID_ARG; misaligned -> ALIGNMENT; workspace too small ->
+ * BUFFER_TOO_SMALL. */
+enum { NVFP4_LOGITS_BF16 = 0, NVFP4_LOGITS_F16 = 1, NVFP4_LOGITS_F32 = 2 };
+int64_t nvfp4_sample_workspace_bytes(int64_t B, int64_t V); /* < 0 if invalid */
+nvfp4_status nvfp4_sample(const void* logits, int64_t ld, int type, int64_t B, int64_t V, const float* u,
+                          const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                          int32_t* tokens, float* logprobs, void* workspace, int64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -27,7 +27,9 @@ __all__ = ["repack", "repack_bytes", "gemm", "gemm_variant", "grouped_gemm", "de
            "gemm_mxfp4", "gemm_variant_mxfp4", "grouped_gemm_mxfp4", "VARIANT_AUTO", "VARIANT_SMALL_M", "VARIANT_LARGE_M", "VARIANT_MFMA", "VARIANT_RESIDENT",
            "VARIANT_MFMA_QUARTER", "VARIANT_KERNELS", "LIB_PATH",
            "rms_norm", "rms_norm_fp8", "rope", "rope_pair_axis", "kv_cache", "kv_write", "rope_kv_write", "kv_read",
-           "paged_attention", "paged_attention_workspace_bytes"]
+           "paged_attention", "paged_attention_workspace_bytes",
+           "KvPlan", "kv_plan", "lora_add", "lora_workspace_bytes", "moe_layer", "moe_layer_workspace_bytes", "sample",
+           "sample_workspace_bytes"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnvfp4_w4a16.so")
 VARIANT_AUTO, VARIANT_SMALL_M, VARIANT_LARGE_M, VARIANT_MFMA, VARIANT_RESIDENT = 0, 1, 2, 3, 4
@@ -120,9 +122,13 @@ def lib() -> ctypes.CDLL:
         L.nvfp4_w4a16_grouped_gemm_variant.argtypes = [P, I64, I64, P, P, P, P, P, I, I, P, I64, I64, I64, I64, I64,
                                                        I, I, I, P]
         L.nvfp4_w4a16_grouped_gemm_variant.restype = I
-        # (the attention half's calls are bound in csrc/binding.cpp)
+        # (the calls of the attention half and around a step's layers are bound in csrc/binding.cpp)
         L.nvfp4_paged_attention_workspace_bytes.argtypes = [I64, I64, I64, I64, I64]
         L.nvfp4_paged_attention_workspace_bytes.restype = I64
+        L.nvfp4_kv_plan_workspace_bytes.argtypes, L.nvfp4_kv_plan_workspace_bytes.restype = [I64, I64], I64
+        L.nvfp4_lora_workspace_bytes.argtypes, L.nvfp4_lora_workspace_bytes.restype = [I64] * 4, I64
+        L.nvfp4_moe_layer_workspace_bytes.argtypes, L.nvfp4_moe_layer_workspace_bytes.restype = [I64] * 5, I64
+        L.nvfp4_sample_workspace_bytes.argtypes, L.nvfp4_sample_workspace_bytes.restype = [I64, I64], I64
         _lib = L
     return _lib
 
@@ -591,3 +597,5 @@ def moe_combine(y, token_row, topk_weights, out=None):
 
 from .attention import (kv_cache, kv_read, kv_write, paged_attention, paged_attention_workspace_bytes,  # noqa: E402
                         rms_norm, rms_norm_fp8, rope, rope_kv_write, rope_pair_axis)
+from .step import (KvPlan, kv_plan, lora_add, lora_workspace_bytes, moe_layer, moe_layer_workspace_bytes,  # noqa: E402
+                   sample, sample_workspace_bytes)

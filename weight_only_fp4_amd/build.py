@@ -1,4 +1,4 @@
-"""Build the HIP library ``libnvfp4_w4a16.so`` in-tree for gfx950, and the Python binding of its attention half.
+"""Build the HIP library ``libnvfp4_w4a16.so`` in-tree for gfx950, and the Python binding of a decode step's calls.
 
     python -m weight_only_fp4_amd.build
 """
@@ -19,7 +19,7 @@ else:   # run as a script
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libnvfp4_w4a16.so")
-BINDING = os.path.join(HERE, "_attention.so")   # Python binding of the attention half, linked against LIB
+BINDING = os.path.join(HERE, "_attention.so")   # Python binding of a decode step's calls, linked against LIB
 ARCH = "gfx950"
 
 COMMON = [
@@ -37,6 +37,10 @@ SOURCES = [
     ("nvfp4_w4a16.hip", VGPR_FORM, "abi"),
     ("nvfp4_mfma.hip", [], "mfma_plan"),
     ("nvfp4_attention.hip", VGPR_FORM, "attention"),
+    ("kv_plan.hip", [], "kv_plan"),
+    ("sample.hip", [], "sample"),
+    ("lora.hip", VGPR_FORM, "lora"),
+    ("moe_few.hip", VGPR_FORM, "moe_few"),
 ] + [
     # single-token attention, one unit per cache format (bf16, fp16, E4M3, NVFP4)
     ("attn.hip", VGPR_FORM + [f"-DNVFP4_KV_FMT={fmt}"], f"attn_{fmt}") for fmt in range(4)

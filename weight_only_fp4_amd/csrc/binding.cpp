@@ -1,6 +1,7 @@
-// Python binding of the attention half of a decoder layer (the calls declared
-// in the last section of include/nvfp4_w4a16.h): checks of the tensors, the
-// outputs' allocation and the descriptors, then one library call.
+// Python binding of the attention half of a decoder layer and of what a decode
+// step runs around its layers (binding_step.h), the calls declared in the last
+// two sections of include/nvfp4_w4a16.h: checks of the tensors, the outputs'
+// allocation and the descriptors, then one library call.
 //
 // These operators take a few microseconds on the GPU when a step has few
 // tokens, and a layer makes several of them, so the marshalling is compiled:
@@ -8,8 +9,8 @@
 // us the current stream, 0.5 us a tensor's checks, 3.9 us the call with its
 // launch), from here 4 to 6 us, most of it the launch.
 //
-// Every function takes its arguments positionally (attention.py has the
-// signatures); wrong ones raise ValueError, a refusal by the library
+// Every function takes its arguments positionally (attention.py and step.py have
+// the signatures); wrong ones raise ValueError, a refusal by the library
 // Nvfp4Error.
 #include <Python.h>
 
@@ -47,7 +48,8 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
 bool is_act(at::ScalarType t) { return t == at::kBFloat16 || t == at::kHalf; }
 
 void unit_stride(const at::Tensor& t, const char* name) {
-    TORCH_CHECK_VALUE(t.dim() == 0 || t.size(-1) <= 1 || t.stride(-1) == 1, name, " must have unit stride in its last dim");
+    TORCH_CHECK_VALUE(t.dim() == 0 || t.size(-1) <= 1 || t.stride(-1) == 1 || t.numel() == 0, name,
+                      " must have unit stride in its last dim");
 }
 
 // The tensor a call's type and device come from: bf16 or fp16, `dim` dims.
@@ -330,6 +332,8 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+#include "binding_step.h"
+
 // set_error(class): what a refusal by the library raises
 PyObject* set_error(PyObject*, PyObject* cls) {
     Py_XINCREF(cls);
@@ -340,6 +344,7 @@ PyObject* set_error(PyObject*, PyObject* cls) {
 
 #define FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(rms_norm), FAST(rope), FAST(kv_append), FAST(kv_read), FAST(paged_attention),
+                         FAST(kv_plan), FAST(lora_add), FAST(moe_layer), FAST(sample),
                          {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attention", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

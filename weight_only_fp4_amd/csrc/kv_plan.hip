@@ -1,0 +1,92 @@
+// C ABI of the page tables and slots of a step (include/nvfp4_w4a16.h).
+#include <hip/hip_runtime.h>
+
+#include "../../include/nvfp4_w4a16.h"
+#include "kernels_plan.h"
+#include "plan.h"
+
+using namespace nvfp4;
+
+namespace {
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+constexpr int64_t kMost = (int64_t)1 << 30;   // requests, rows and tokens of a table's row stay below
+
+// Rows written by the scans' own workgroup.
+constexpr int64_t kPlanOneLaunch = 4096;
+
+bool one_launch(int64_t B, int64_t T) { return B <= kPlanLds && T <= kPlanOneLaunch; }
+
+}  // namespace
+
+extern "C" {
+
+int64_t nvfp4_kv_plan_workspace_bytes(int64_t B, int64_t T) {
+    if (B < 0 || B >= kMost || T < 0 || T >= kMost) {
+        fail(NVFP4_ERR_INVALID_ARG, "nvfp4_kv_plan_workspace_bytes: B = %lld, T = %lld", (long long)B, (long long)T);
+        return -1;
+    }
+    return one_launch(B, T) ? 0 : B * (int64_t)sizeof(int2);
+}
+
+nvfp4_status nvfp4_kv_plan(const int32_t* cached, const int32_t* fresh, int64_t B, int32_t* page_table, int64_t ld_table,
+                           int64_t max_pages, int64_t page_size, const int32_t* free_pages, int64_t F, const int32_t* head,
+                           int64_t T, int32_t* slots, int32_t* positions, int32_t* requests, int32_t* lengths,
+                           int32_t* offsets, int32_t* head_out, void* workspace, int64_t workspace_bytes, void* stream) {
+    const char* fn = "nvfp4_kv_plan";
+    if (B < 0 || B >= kMost || T < 0 || T >= kMost)
+        return fail(NVFP4_ERR_INVALID_ARG, "%s: B = %lld, T = %lld must be in [0, 2^30)", fn, (long long)B, (long long)T);
+    if (page_size < 1 || page_size >= kMost || max_pages < 0 || max_pages >= kMost || max_pages * page_size >= kMost)
+        return fail(NVFP4_ERR_INVALID_ARG, "%s: max_pages = %lld of page_size = %lld: a table's row must hold fewer than 2^30 tokens",
+                    fn, (long long)max_pages, (long long)page_size);
+    if (ld_table < max_pages || ld_table >= (int64_t)1 << 40)
+        return fail(NVFP4_ERR_INVALID_ARG, "%s: ld_table = %lld < max_pages = %lld or too large", fn, (long long)ld_table,
+                    (long long)max_pages);
+    if (F < 0 || F >= (int64_t)1 << 31) return fail(NVFP4_ERR_INVALID_ARG, "%s: F = %lld free pages", fn, (long long)F);
+    if (!head || !head_out || !offsets || (F > 0 && !free_pages) || (B > 0 && (!cached || !fresh || !lengths)) ||
+        (B > 0 && max_pages > 0 && !page_table) || (T > 0 && (!slots || !positions || !requests)))
+        return fail(NVFP4_ERR_INVALID_ARG, "%s: NULL pointer", fn);
+    const void* all[] = {cached, fresh, page_table, free_pages, head, slots, positions, requests, lengths, offsets, head_out};
+    for (const void* p : all)
+        if (!aligned(p, 4)) return fail(NVFP4_ERR_ALIGNMENT, "%s: int32 arrays must be 4-byte aligned", fn);
+    const int64_t need = nvfp4_kv_plan_workspace_bytes(B, T);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need)
+            return fail(NVFP4_ERR_BUFFER_TOO_SMALL, "%s: workspace of %lld bytes is below the %lld bytes this call needs", fn,
+                        (long long)workspace_bytes, (long long)need);
+        if (!aligned(workspace, 8)) return fail(NVFP4_ERR_ALIGNMENT, "%s: workspace must be 8-byte aligned", fn);
+    }
+    PlanArgs a;
+    a.cached = cached;
+    a.fresh = fresh;
+    a.table = page_table;
+    a.ld_table = ld_table;
+    a.free_pages = free_pages;
+    a.head = head;
+    a.slots = slots;
+    a.positions = positions;
+    a.requests = requests;
+    a.lengths = lengths;
+    a.offsets = offsets;
+    a.head_out = head_out;
+    a.seen = static_cast<int2*>(workspace);
+    a.F = F;
+    a.page_limit = ((int64_t)1 << 31) / page_size;
+    a.B = (int)B;
+    a.width = (int)max_pages;
+    a.page = (int)page_size;
+    a.T = (int)T;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (one_launch(B, T)) {
+        hipLaunchKernelGGL((k_plan<true>), dim3(1), dim3(kPlanThreads), 0, st, a);
+        return launched(fn);
+    }
+    hipLaunchKernelGGL((k_plan<false>), dim3(1), dim3(kPlanThreads), 0, st, a);
+    nvfp4_status s = launched(fn);
+    if (s != NVFP4_OK || T == 0) return s;
+    hipLaunchKernelGGL(k_plan_rows, dim3((unsigned)((T + kPlanRows - 1) / kPlanRows)), dim3(256), 0, st, a);
+    return launched(fn);
+}
+
+}  // extern "C"

@@ -1,0 +1,131 @@
+// C ABI of the low-rank adapters (include/nvfp4_w4a16.h).
+#include <hip/hip_runtime.h>
+
+#include "../../include/nvfp4_w4a16.h"
+#include "kernels_lora.h"
+#include "plan.h"
+
+using namespace nvfp4;
+
+namespace {
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+constexpr int64_t kFar = (int64_t)1 << 40;
+
+bool sizes(const char* fn, int64_t T, int64_t K, int64_t N, int64_t R) {
+    // row tiles are the grid's second axis
+    if (T < 0 || T > (int64_t)65535 * kLoraRows || K < 8 || K >= (int64_t)1 << 24 || K % 8 != 0 || N < 0 || N >= (int64_t)1 << 24) {
+        fail(NVFP4_ERR_INVALID_ARG, "%s: T = %lld must be in [0, 1048560], K = %lld a multiple of 8 in [8, 2^24), N = %lld in [0, 2^24)",
+             fn, (long long)T, (long long)K, (long long)N);
+        return false;
+    }
+    if (R < 8 || R > kLoraMaxRank || R % 8 != 0) {
+        fail(NVFP4_ERR_INVALID_ARG, "%s: rank %lld must be a multiple of 8 up to %d", fn, (long long)R, kLoraMaxRank);
+        return false;
+    }
+    return true;
+}
+
+// Rows up to which each of a tile's adapters gets its own workgroups (their
+// grid's third axis); beyond, a workgroup takes them one after another.
+constexpr int64_t kLoraApart = 256;
+
+struct LoraShape {
+    int slices, slice, places;
+};
+LoraShape lora_shape(int64_t T, int64_t K, int64_t L) {
+    LoraShape s;
+    const int64_t tiles = (T + kLoraRows - 1) / kLoraRows;
+    s.places = T <= kLoraApart ? (int)(L < kLoraRows ? (L < 1 ? 1 : L) : kLoraRows) : 1;
+    // slices of at least a chunk for each wave, as many as make about 512 workgroups of tiles with all their places
+    int64_t want = (512 + tiles * s.places - 1) / (tiles * s.places);
+    if (want < 1) want = 1;
+    const int64_t most = (K + 511) / 512;
+    if (want > most) want = most;
+    if (want > 16) want = 16;
+    s.slice = (int)round_up((K + want - 1) / want, 128);
+    s.slices = (int)((K + s.slice - 1) / s.slice);
+    return s;
+}
+
+template <bool F16>
+void launch(const LoraArgs& a, const LoraShape& s, hipStream_t st) {
+    const int tiles = (a.T + kLoraRows - 1) / kLoraRows;
+    const dim3 down((unsigned)a.slices, (unsigned)tiles, (unsigned)s.places), block(kLoraThreads);
+    const int per = kLoraWaves * kLoraCols;
+    const dim3 up((unsigned)((a.N + per - 1) / per), (unsigned)tiles, (unsigned)s.places);
+    if (a.R <= 16) hipLaunchKernelGGL((k_lora_down<1, F16>), down, block, 0, st, a);
+    else if (a.R <= 32) hipLaunchKernelGGL((k_lora_down<2, F16>), down, block, 0, st, a);
+    else if (a.R <= 64) hipLaunchKernelGGL((k_lora_down<4, F16>), down, block, 0, st, a);
+    else hipLaunchKernelGGL((k_lora_down<8, F16>), down, block, 0, st, a);
+    if (a.R <= 32) hipLaunchKernelGGL((k_lora_up<1, F16>), up, block, 0, st, a);
+    else if (a.R <= 64) hipLaunchKernelGGL((k_lora_up<2, F16>), up, block, 0, st, a);
+    else hipLaunchKernelGGL((k_lora_up<4, F16>), up, block, 0, st, a);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t nvfp4_lora_workspace_bytes(int64_t T, int64_t K, int64_t N, int64_t R) {
+    if (!sizes("nvfp4_lora_workspace_bytes", T, K, N, R)) return -1;
+    // the most slices that any number of adapters gives
+    return T == 0 || N == 0 ? 0 : (int64_t)lora_shape(T, K, 1).slices * T * R * 4;
+}
+
+nvfp4_status nvfp4_lora_add(const void* x, int64_t ld_x, const void* a, int64_t a_l, int64_t a_r, const void* b, int64_t b_l,
+                            int64_t b_n, const int32_t* adapter, const float* scale, const void* y, int64_t ld_y, void* out,
+                            int64_t ld_o, int64_t T, int64_t K, int64_t N, int64_t R, int64_t L, void* workspace,
+                            int64_t workspace_bytes, int f16, void* stream) {
+    const char* fn = "nvfp4_lora_add";
+    if (!sizes(fn, T, K, N, R)) return NVFP4_ERR_INVALID_ARG;
+    if (L < 0 || L >= (int64_t)1 << 31) return fail(NVFP4_ERR_INVALID_ARG, "%s: L = %lld adapters", fn, (long long)L);
+    if (T == 0 || N == 0) return ok();
+    if (ld_x < K || ld_y < N || ld_o < N || ld_x >= kFar || ld_y >= kFar || ld_o >= kFar)
+        return fail(NVFP4_ERR_INVALID_ARG, "%s: a leading dimension is below its row's length or too large", fn);
+    if (a_l < 0 || a_r < 0 || b_l < 0 || b_n < 0 || a_l >= kFar || a_r >= kFar || b_l >= kFar || b_n >= kFar)
+        return fail(NVFP4_ERR_INVALID_ARG, "%s: strides of a or b are out of range", fn);
+    if (!x || !y || !out || !adapter || (L > 0 && (!a || !b))) return fail(NVFP4_ERR_INVALID_ARG, "%s: NULL pointer", fn);
+    if (!aligned(x, 16) || ld_x % 8 != 0 || !aligned(a, 16) || a_l % 8 != 0 || a_r % 8 != 0 || !aligned(b, 16) ||
+        b_l % 8 != 0 || b_n % 8 != 0)
+        return fail(NVFP4_ERR_ALIGNMENT, "%s: rows of x, a and b must be 16-byte aligned", fn);
+    if (!aligned(y, 2) || !aligned(out, 2) || !aligned(adapter, 4) || !aligned(scale, 4))
+        return fail(NVFP4_ERR_ALIGNMENT, "%s: misaligned pointer", fn);
+    const int64_t need = nvfp4_lora_workspace_bytes(T, K, N, R);
+    if (!workspace || workspace_bytes < need)
+        return fail(NVFP4_ERR_BUFFER_TOO_SMALL, "%s: workspace of %lld bytes is below the %lld bytes this call needs", fn,
+                    (long long)workspace_bytes, (long long)need);
+    if (!aligned(workspace, 16)) return fail(NVFP4_ERR_ALIGNMENT, "%s: workspace must be 16-byte aligned", fn);
+    const LoraShape s = lora_shape(T, K, L);
+    LoraArgs g;
+    g.x = static_cast<const uint16_t*>(x);
+    g.a = static_cast<const uint16_t*>(a);
+    g.b = static_cast<const uint16_t*>(b);
+    g.y = static_cast<const uint16_t*>(y);
+    g.out = static_cast<uint16_t*>(out);
+    g.adapter = adapter;
+    g.scale = scale;
+    g.h = static_cast<float*>(workspace);
+    g.ld_x = ld_x;
+    g.ld_y = ld_y;
+    g.ld_o = ld_o;
+    g.a_l = a_l;
+    g.a_r = a_r;
+    g.b_l = b_l;
+    g.b_n = b_n;
+    g.T = (int)T;
+    g.K = (int)K;
+    g.N = (int)N;
+    g.R = (int)R;
+    g.L = (int)L;
+    g.slices = s.slices;
+    g.slice = s.slice;
+    g.vec = aligned(y, 16) && aligned(out, 16) && ld_y % 8 == 0 && ld_o % 8 == 0;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (f16) launch<true>(g, s, st);
+    else launch<false>(g, s, st);
+    return launched(fn);
+}
+
+}  // extern "C"
