@@ -739,14 +739,14 @@ nvfp4_status nvfp4_moe_layer(const void* x, int64_t ld_x, const int32_t* topk_id
  * 0, above it as the last), and logprobs[b] = ln(w / total).  t <= 0 or NaN: the
  * first largest, logprob 0.  A row of -infinities: token -1, logprob -infinity.
  * A largest logit of +infinity leaves only those that equal it.
- * The weights are computed in fp64 and rounded to multiples of 2^-s, s = min(52,
- * 62 - ceil(log2 V)): sums are exact and results do not depend on timing.
+ * The weights are computed in fp64 and rounded to multiples of 2^-s, s = min(45,
+ * 62 - ceil(log2 V)), or of less; sums do not depend on timing.
  *   u fp32 [B]; temperature (NULL: 1), top_p, min_p fp32 [B], top_k int32 [B]
  *   (NULL: off); tokens int32 [B]; logprobs fp32 [B] or NULL.  Rows of logits
  *   need only their type's alignment, and may share memory (ld below V).
  *   workspace: nvfp4_sample_workspace_bytes(B, V) bytes, 256-byte aligned, any
  *   contents.
- * B == 0 launches nothing.  Errors: sizes (B < 2^22, V in [1, 2^23], ld < 0),
+ * B == 0 launches nothing.  Errors: sizes (B <= 65535, V in [1, 2^23], ld < 0),
  * NULL pointers -> INVALID_ARG; misaligned -> ALIGNMENT; workspace too small ->
  * BUFFER_TOO_SMALL. */
 enum { NVFP4_LOGITS_BF16 = 0, NVFP4_LOGITS_F16 = 1, NVFP4_LOGITS_F32 = 2 };

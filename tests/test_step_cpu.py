@@ -102,11 +102,12 @@ def test_moe_layer_refusals(L, kw, status, needle):
 
 
 @pytest.mark.parametrize("kw,status,needle", [
-    (dict(B=-1), INVALID, "B ="), (dict(B=1 << 22), INVALID, "B ="), (dict(V=0), INVALID, "V ="), (dict(V=(1 << 23) + 1), INVALID, "V ="),
+    (dict(B=-1), INVALID, "B ="), (dict(B=65536), INVALID, "B ="), (dict(V=0), INVALID, "V ="), (dict(V=(1 << 23) + 1), INVALID, "V ="),
     (dict(type=3), INVALID, "type"), (dict(type=-1), INVALID, "type"), (dict(ld=-1), INVALID, "ld ="), (dict(x=None), INVALID, "NULL"),
     (dict(u=None), INVALID, "NULL"), (dict(o=None), INVALID, "NULL"), (dict(x=A + 1), ALIGN, "logits"),
     (dict(type=2, x=A + 2), ALIGN, "logits"), (dict(u=A + 2), ALIGN, "4-byte"), (dict(t=A + 2), ALIGN, "4-byte"),
-    (dict(o=A + 2), ALIGN, "4-byte"), (dict(lp=A + 1), ALIGN, "4-byte"), (dict(B=0), OK, ""), (dict(B=0, x=None, u=None), OK, ""),
+    (dict(o=A + 2), ALIGN, "4-byte"), (dict(lp=A + 1), ALIGN, "4-byte"), (dict(ws=None), SMALL, "workspace"),
+    (dict(wsb=1000), SMALL, "workspace"), (dict(ws=A + 16), ALIGN, "workspace"), (dict(B=0), OK, ""), (dict(B=0, x=None, u=None), OK, ""),
 ])
 def test_sample_refusals(L, kw, status, needle):
     a = dict(x=A, ld=100, type=0, B=4, V=100, u=A, t=A, k=A, p=A, mp=A, o=A, lp=A, ws=A, wsb=1 << 30)
