@@ -47,6 +47,7 @@ constexpr int kSampleBins = 512;
 constexpr float kSamplePerUnit = 16.f; // bins a unit of (m - l) / t
 constexpr int kSampleListed = 2048;    // elements a slice lists
 constexpr int kSampleList = 4096;      // elements k_sample_pick sorts
+constexpr int kSampleNarrow = 256;     // above which it narrows them down first
 constexpr int kSampleMaxSlices = 64;
 constexpr int kSampleHeld = 4;         // pieces that a thread of k_sample_scan holds
 
@@ -106,6 +107,7 @@ template <int DT>
 struct SampleRow {
     const uint8_t* base;   // the first piece, aligned down
     int skew, V, pieces;
+    int full0, full1;      // pieces that lie wholly in the row
     __device__ __forceinline__ SampleRow(const SampleArgs& a, int b) {
         const uint8_t* p = static_cast<const uint8_t*>(a.logits) + (int64_t)b * a.ld * Logit<DT>::kSize;
         const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15);
@@ -113,6 +115,8 @@ struct SampleRow {
         skew = off / Logit<DT>::kSize;
         V = a.V;
         pieces = (skew + V + Logit<DT>::kPiece - 1) / Logit<DT>::kPiece;
+        full0 = skew > 0 ? 1 : 0;
+        full1 = (skew + V) / Logit<DT>::kPiece;
     }
     template <typename F>
     __device__ __forceinline__ void piece(int c, F&& f) const {
@@ -137,27 +141,42 @@ struct SampleRow {
     }
 };
 
-// A piece as it lies in memory, places outside the row as NaN, which counts for
-// nothing anywhere, as a logit that is NaN does.
-template <int DT>
-__device__ __forceinline__ uint4 sample_load(const SampleRow<DT>& row, int c, int end) {
+// Pieces c, c + step, .. below `end` as they lie in memory; places outside the
+// row are NaN, which counts for nothing anywhere, as a logit that is NaN does.
+// The loads are unconditional (from a whole piece of the row) and all in flight
+// before the few that are cut by the row's ends are put right.
+template <int DT, int N>
+__device__ __forceinline__ void sample_load(const SampleRow<DT>& row, int c, int step, int end, uint4 (&v)[N]) {
     constexpr int P = Logit<DT>::kPiece;
-    const int i0 = c * P - row.skew;
-    const uint8_t* p = row.base + (int64_t)c * 16;
-    if (c < end && i0 >= 0 && i0 + P <= row.V) return *reinterpret_cast<const uint4*>(p);
-    uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};
-    if (c < end) {
+    const bool any = row.full1 > row.full0;   // the same in all threads
+    if (any) {
 #pragma unroll
-        for (int e = 0; e < P; ++e) {
-            if (i0 + e < 0 || i0 + e >= row.V) continue;
-            if (DT == kLogitF32) w[e & 3] = reinterpret_cast<const uint32_t*>(p)[e];
-            else {
-                const uint32_t x = reinterpret_cast<const uint16_t*>(p)[e];
-                w[(e >> 1) & 3] = (e & 1) ? (w[(e >> 1) & 3] & 0xFFFFu) | x << 16 : (w[(e >> 1) & 3] & 0xFFFF0000u) | x;
-            }
+        for (int h = 0; h < N; ++h) {
+            int at = c + h * step;
+            at = at < row.full0 ? row.full0 : at >= row.full1 ? row.full1 - 1 : at;
+            v[h] = *reinterpret_cast<const uint4*>(row.base + (int64_t)at * 16);
         }
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+    for (int h = 0; h < N; ++h) {
+        const int at = c + h * step;
+        if (at >= row.full0 && at < row.full1 && at < end) continue;
+        uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};
+        if (at < end) {
+            const uint8_t* p = row.base + (int64_t)at * 16;
+            const int i0 = at * P - row.skew;
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+                if (i0 + e < 0 || i0 + e >= row.V) continue;
+                if (DT == kLogitF32) w[e & 3] = reinterpret_cast<const uint32_t*>(p)[e];
+                else {
+                    const uint32_t x = reinterpret_cast<const uint16_t*>(p)[e];
+                    w[(e >> 1) & 3] = (e & 1) ? (w[(e >> 1) & 3] & 0xFFFFu) | x << 16 : (w[(e >> 1) & 3] & 0xFFFF0000u) | x;
+                }
+            }
+        }
+        v[h] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
 }
 // f(place e, value) of a loaded piece's logits (NaN among them).
 template <int DT, typename F>
@@ -226,7 +245,7 @@ template <typename T>
 __device__ __forceinline__ T sample_scan(T v, uint64_t* sums, T& total) {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     uint64_t x = (uint64_t)v;
-#pragma unroll
+#pragma unroll 1
     for (int d = 1; d < 64; d <<= 1) {
         const uint64_t o = shfl_up_u64(x, d);
         if (lane >= d) x += o;
@@ -253,6 +272,7 @@ struct SampleCut {
 
 struct SampleShared {
     uint64_t digits[256 * kSampleCopies];   // counters or weights of the digits; of the row's steps in the draw; a list
+    uint64_t second[kSampleList];
     uint64_t sums[kSampleWaves];
     uint64_t above;    // of the digits above the chosen one
     double fsums[kSampleWaves];
@@ -264,6 +284,7 @@ struct SampleShared {
     int digit;
     int found;
     int count;
+    uint32_t low, high;
 };
 static_assert(256 * kSampleCopies == kSampleList, "the digits' room holds a list");
 
@@ -357,9 +378,11 @@ struct SampleSettings {
     }
 };
 
-// One row by one workgroup, everything from the row itself.
+// One row by one workgroup, everything from the row itself.  Out of line: few
+// rows come here, and the others' registers and instruction fetches stay free
+// of it.
 template <int DT>
-__device__ __forceinline__ void sample_slow(const SampleArgs& a, int b, float largest, SampleShared& sh) {
+__device__ __noinline__ void sample_slow(SampleArgs a, int b, float largest, SampleShared& sh) {
     const int tid = threadIdx.x;
     const SampleRow<DT> row(a, b);
     const SampleSettings set(a, b);
@@ -446,7 +469,7 @@ __device__ __forceinline__ int sample_listed_bins(const SampleSettings& set) {
 }
 
 // Grid: (slices, rows).  A thread's pieces are 256 apart; a slice of up to
-// 1024 is read once and stays in registers.
+// 1024 is read once and stays in LDS.
 template <int DT>
 __global__ void __launch_bounds__(kSampleScanThreads) k_sample_scan(SampleArgs a) {
     constexpr int P = Logit<DT>::kPiece;
@@ -457,12 +480,14 @@ __global__ void __launch_bounds__(kSampleScanThreads) k_sample_scan(SampleArgs a
     const int tid = threadIdx.x, lane = tid & 63, s = blockIdx.x, b = blockIdx.y;
     const SampleRow<DT> row(a, b);
     const int c0 = s * a.slice, c1 = c0 + a.slice < row.pieces ? c0 + a.slice : row.pieces;
-    uint4 held[kSampleHeld];
-    auto load = [&](int c) {
-#pragma unroll
-        for (int h = 0; h < kSampleHeld; ++h) held[h] = sample_load(row, c + tid + h * kSampleScanThreads, c1);
-    };
     constexpr int kAtOnce = kSampleHeld * kSampleScanThreads;
+    __shared__ uint4 s_held[kAtOnce];   // a thread reads what it wrote itself
+    auto load = [&](int c) {
+        uint4 v[kSampleHeld];
+        sample_load<DT, kSampleHeld>(row, c + tid, kSampleScanThreads, c1, v);
+#pragma unroll
+        for (int h = 0; h < kSampleHeld; ++h) s_held[h * kSampleScanThreads + tid] = v[h];
+    };
     load(c0);
     const SampleSettings set(a, b);
     SampleSlice& out = a.slices[(int64_t)b * a.S + s];
@@ -470,10 +495,10 @@ __global__ void __launch_bounds__(kSampleScanThreads) k_sample_scan(SampleArgs a
     auto all = [&](auto&& f) {
         for (int c = c0; c < c1; c += kAtOnce) {
             if (a.slice > kAtOnce) load(c);
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < kSampleHeld; ++h) {
                 const int i0 = (c + tid + h * kSampleScanThreads) * P - row.skew;
-                sample_values<DT>(held[h], [&](int e, float l) { f(i0 + e, l); });
+                sample_values<DT>(s_held[h * kSampleScanThreads + tid], [&](int e, float l) { f(i0 + e, l); });
             }
         }
     };
@@ -587,7 +612,7 @@ __device__ __forceinline__ void sample_sort(uint64_t* list, int n) {
 // Inclusive scan of doubles over the workgroup, in a fixed order.
 __device__ __forceinline__ double sample_scan_f64(double v, double* sums, double& total) {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-#pragma unroll
+#pragma unroll 1
     for (int d = 1; d < 64; d <<= 1) {
         const double o = __shfl_up(v, d);
         if (lane >= d) v += o;
@@ -613,23 +638,21 @@ __device__ __forceinline__ int sample_fill(uint64_t* list, int n) {
     return size;
 }
 
-// Bin d of the row from the slices': f(slice, content), eight loads in flight.
+// Bin d of the row from the slices': f(slice, content), sixteen loads in flight.
 template <typename F>
 __device__ __forceinline__ void sample_join(const SampleSlice* slices, int S, const SampleShared& sh, int d, F&& f) {
-    for (int s0 = 0; s0 < S; s0 += 8) {
-        uint64_t v[8];
+    for (int s0 = 0; s0 < S; s0 += 16) {
+        uint64_t v[16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 16; ++i) {
             const int s = s0 + i < S ? s0 + i : S - 1, at = d - sh.below[s];
             v[i] = slices[s].bins[at > 0 ? at : 0];
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 16; ++i)
             if (s0 + i < S && d >= sh.below[s0 + i]) f(s0 + i, v[i]);
     }
 }
-
-constexpr int kSampleEach = kSampleList / kSampleThreads;   // elements of a full list a thread has
 
 // Rows whose slices made lists; false: a list was too long.
 template <int DT>
@@ -672,78 +695,57 @@ __device__ __forceinline__ bool sample_listed(const SampleArgs& a, int b, const 
     if (n > kSampleList) return false;
     const int size = sample_fill(list, n);
     sample_sort(list, size);
-    // a thread's elements are neighbours
+    // a thread's elements are neighbours: i0 .. i1 (the loops stay loops: most
+    // lists give a thread one, and code that runs once costs its fetch)
     const int each = (size + kSampleThreads - 1) / kSampleThreads;
     const int left = set.k > 0 && set.k < n ? set.k : n;   // after top-k
-    uint64_t q[kSampleEach], sum = 0, total;
-    double wt[kSampleEach];
-#pragma unroll
-    for (int e = 0; e < kSampleEach; ++e) {
-        const int i = tid * each + e;
-        const bool in = e < each && i < left;
-        wt[e] = in ? sw.weight(sample_value((uint32_t)(list[in ? i : 0] >> 32)), sw.shift) : 0.0;
-        q[e] = SampleWeights::rounded(wt[e]);
-        sum += q[e];
+    auto units = [&](uint64_t key) { return sw.units(sample_value((uint32_t)key)); };
+    int i0 = tid * each, i1 = i0 + each < left ? i0 + each : left;
+    uint64_t sum = 0, total;
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) sum += units(list[i] >> 32);
+    uint64_t run = sample_scan<uint64_t>(sum, sh.sums, total) - sum;
+    const double target = (double)set.p * (double)total;
+    uint64_t kept = 0, all;
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) {
+        const float l = sample_value((uint32_t)(list[i] >> 32));
+        if (i == 0 || ((!(set.p < 1.f) || (double)run < target) && set.keeps(sw.weight(l)))) ++kept;
+        run += units(list[i] >> 32);
     }
-    const uint64_t upto = sample_scan<uint64_t>(sum, sh.sums, total);
-    uint64_t run = upto - sum, kept = 0;
-    const double target = (double)set.p * (double)total, per = 1.0 / sw.unit();
-#pragma unroll
-    for (int e = 0; e < kSampleEach; ++e) {
-        const int i = tid * each + e;
-        const bool in = e < each && i < left;
-        if (in && (i == 0 || ((!(set.p < 1.f) || (double)run < target) && set.keeps(wt[e] * per)))) ++kept;
-        run += q[e];
-    }
-    uint64_t all;
     sample_scan<uint64_t>(kept, sh.sums, all);   // what is kept is a prefix: its length
     const int m = (int)all;
     // the kept ones by index (ascending: the complement descends), with their keys
-    uint64_t mine[kSampleEach];
-#pragma unroll
-    for (int e = 0; e < kSampleEach; ++e) {
-        const int i = tid + e * kSampleThreads;
-        mine[e] = i < m ? list[i] : 0;
-    }
-    __syncthreads();
-    const int size2 = sample_fill(list, m);
-#pragma unroll
-    for (int e = 0; e < kSampleEach; ++e) {
-        const int i = tid + e * kSampleThreads;
-        if (i < m) list[i] = mine[e] << 32 | mine[e] >> 32;   // (~index, key)
-    }
-    sample_sort(list, size2);
+    uint64_t* by_index = sh.second;
+    for (int i = tid; i < m; i += kSampleThreads) by_index[i] = list[i] << 32 | list[i] >> 32;   // (~index, key)
+    sample_sort(by_index, sample_fill(by_index, m));
     sum = 0;
-#pragma unroll
-    for (int e = 0; e < kSampleEach; ++e) {
-        const int i = tid * each + e;
-        const bool in = e < each && i < m;
-        q[e] = in ? sw.units(sample_value((uint32_t)list[in ? i : 0])) : 0;
-        sum += q[e];
-    }
+    i1 = i0 + each < m ? i0 + each : m;
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) sum += units(by_index[i]);
     const uint64_t end = sample_scan<uint64_t>(sum, sh.sums, total);
     run = end - sum;
     const uint64_t aim = set.aim(total);
     if (end > aim && run <= aim) {
-        bool done = false;
-#pragma unroll
-        for (int e = 0; e < kSampleEach; ++e) {
-            run += q[e];
-            if (!done && run > aim) {
-                done = true;
-                const uint64_t x = list[tid * each + e];
-                a.tokens[b] = (int)~(uint32_t)(x >> 32);
-                if (a.logprobs) a.logprobs[b] = sw.logprob(sample_value((uint32_t)x), (double)total / sw.unit());
-            }
-        }
+        int i = i0;
+#pragma unroll 1
+        while ((run += units(by_index[i])) <= aim) ++i;
+        a.tokens[b] = (int)~(uint32_t)(by_index[i] >> 32);
+        if (a.logprobs) a.logprobs[b] = sw.logprob(sample_value((uint32_t)by_index[i]), (double)total / sw.unit());
     }
     return true;
 }
 
 // The least fp32 value whose bin is at least `bin`: bins rise with values, so
-// a binary search of the keys.
+// a binary search of the keys, next to the quotient if it is there.
 __device__ __forceinline__ float sample_bin_begin(float bin, float grid) {
     uint32_t lo = kSampleNone, hi = 0xFF800000u;   // the keys of the infinities
+    const uint32_t near = sample_key(bin / grid);
+    if (near > lo + 4 && near < hi - 4 && sample_bin(sample_value(near - 4), grid) < bin &&
+        sample_bin(sample_value(near + 4), grid) >= bin) {
+        lo = near - 3;
+        hi = near + 4;
+    }
     while (lo < hi) {
         const uint32_t mid = lo + (hi - lo) / 2;
         if (sample_bin(sample_value(mid), grid) >= bin) hi = mid;
@@ -809,61 +811,124 @@ __device__ __forceinline__ bool sample_summed(const SampleArgs& a, int b, const 
         const float from = sample_bin_begin(top - (float)hi, grid), to = sample_bin_begin(top - (float)lo + 1.f, grid);
         for (int c = tid; c < row.pieces; c += 4 * kSampleThreads) {
             uint4 v[4];
+            sample_load<DT, 4>(row, c, kSampleThreads, row.pieces, v);
+            uint32_t hits = 0;   // bit h P + e: place e of piece h
 #pragma unroll
-            for (int h = 0; h < 4; ++h) v[h] = sample_load(row, c + h * kSampleThreads, row.pieces);
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                uint32_t hits = 0;
-                sample_values<DT>(v[h], [&](int e, float l) { hits |= (l >= from && l < to ? 1u : 0u) << e; });
-                if (hits == 0) continue;
-                const int i0 = (c + h * kSampleThreads) * P - row.skew;
-                int at = atomicAdd(&sh.count, __popc(hits));
-                sample_values<DT>(v[h], [&](int e, float l) {
-                    if ((hits >> e) & 1u) {
-                        if (at < kSampleList) list[at] = (uint64_t)sample_key(l) << 32 | (uint32_t)~(i0 + e);
-                        ++at;
-                    }
-                });
-            }
+            for (int h = 0; h < 4; ++h)
+                sample_values<DT>(v[h], [&](int e, float l) { hits |= (l >= from && l < to ? 1u : 0u) << (h * P + e); });
+            if (hits == 0) continue;
+            int at = atomicAdd(&sh.count, __popc(hits));
+            do {   // their places: few, so that the values are read again below
+                const int bit = __builtin_ctz(hits);
+                hits &= hits - 1;
+                if (at < kSampleList) list[at] = (uint32_t)((c + bit / P * kSampleThreads) * P + bit % P);
+                ++at;
+            } while (hits);
         }
         __syncthreads();
         above = sh.fsums[0];
     }
-    const int count = sh.count;
-    __syncthreads();
+    int count = sh.count;
     if (count > kSampleList) return false;
+    for (int i = tid; i < count; i += kSampleThreads) {   // place -> (key, index)
+        const int place = (int)list[i];
+        const uint8_t* p = row.base + (int64_t)place * Logit<DT>::kSize;
+        const uint32_t bits = DT == kLogitF32 ? *reinterpret_cast<const uint32_t*>(p) : *reinterpret_cast<const uint16_t*>(p);
+        list[i] = (uint64_t)sample_key(Logit<DT>::value(bits)) << 32 | (uint32_t)~(place - row.skew);
+    }
+    __syncthreads();
     SampleCut cut = {0u, -1};   // the list's last kept element, if any
     if (lo < kSampleBins) {
+        // in units of the row: what is missing to the target above the list
+        double rest = set.p < 1.f ? (target - above) * sw.unit() : 9e18;
+        // A long list is first cut down to the part, of 1024 of its keys' range,
+        // in which its sum reaches the target: those above are kept.
+        if (!set.filters && count > kSampleNarrow) {
+            uint32_t low = ~0u, high = 0;
+            for (int i = tid; i < count; i += kSampleThreads) {
+                const uint32_t k = (uint32_t)(list[i] >> 32);
+                low = k < low ? k : low;
+                high = k > high ? k : high;
+            }
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) {
+                const uint32_t x = __shfl_xor(low, m), y = __shfl_xor(high, m);
+                low = x < low ? x : low;
+                high = y > high ? y : high;
+            }
+            if (tid == 0) {
+                sh.low = ~0u;
+                sh.high = 0;
+                sh.count = 0;
+            }
+            uint64_t* parts = sh.second;
+            parts[tid] = 0;
+            __syncthreads();
+            if (lane == 0) {
+                atomicMin(&sh.low, low);
+                atomicMax(&sh.high, high);
+            }
+            __syncthreads();
+            low = sh.low;
+            high = sh.high;
+            const int shift = 32 - __clz((int)((high - low) >> 10));   // the range is below 2^(10 + shift)
+            auto part = [&](uint64_t x) { return (int)((high - (uint32_t)(x >> 32)) >> shift); };
+            if (tid == 0) sh.digit = part((uint64_t)low << 32);
+#pragma unroll 1
+            for (int i = tid; i < count; i += kSampleThreads)
+                atomicAdd((unsigned long long*)&parts[part(list[i])],
+                          (unsigned long long)sw.units(sample_value((uint32_t)(list[i] >> 32))));
+            __syncthreads();
+            uint64_t all;
+            const uint64_t q = parts[tid], end = sample_scan<uint64_t>(q, sh.sums, all);
+            int first = (double)end >= rest ? tid : kSampleThreads;
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) {
+                const int o = __shfl_xor(first, m);
+                first = o < first ? o : first;
+            }
+            if (lane == 0) atomicMin(&sh.digit, first);
+            __syncthreads();
+            const int chosen = sh.digit;
+            if (tid == chosen) sh.above = end - q;
+            __syncthreads();
+            rest -= (double)sh.above;
+#pragma unroll 1
+            for (int i = tid; i < count; i += kSampleThreads) {
+                const uint64_t x = list[i];
+                const int at = part(x);
+                if (at == chosen) {
+                    sh.second[atomicAdd(&sh.count, 1)] = x;
+                } else if (at < chosen) {
+                    const int of = slice_of(x);
+                    atomicAdd((unsigned long long*)&sh.kept[of],
+                              (unsigned long long)units_in(of, sample_value((uint32_t)(x >> 32))));
+                }
+            }
+            if (chosen > 0) cut = SampleCut{high - ((uint32_t)chosen << shift) + 1u, a.V};
+            __syncthreads();
+            count = sh.count;
+            list = sh.second;
+        }
         const int size = sample_fill(list, count);
         sample_sort(list, size);
         const int each = (size + kSampleThreads - 1) / kSampleThreads;
-        uint64_t q[kSampleEach];
-        int of[kSampleEach];
-        double sum = 0.0, all;
-#pragma unroll
-        for (int e = 0; e < kSampleEach; ++e) {
-            const int i = tid * each + e;
-            q[e] = 0;
-            of[e] = 0;
-            if (e < each && i < count) {
-                of[e] = slice_of(list[i]);
-                q[e] = units_in(of[e], sample_value((uint32_t)(list[i] >> 32)));
-                sum += (double)q[e] * unit * sh.factor[of[e]];
-            }
-        }
-        double run = above + sample_scan_f64(sum, sh.fsums, all) - sum;
+        const int i0 = tid * each, i1 = i0 + each < count ? i0 + each : count;
+        uint64_t sum = 0, all;
+#pragma unroll 1
+        for (int i = i0; i < i1; ++i) sum += sw.units(sample_value((uint32_t)(list[i] >> 32)));
+        uint64_t run = sample_scan<uint64_t>(sum, sh.sums, all) - sum;
         int kept = 0;
-#pragma unroll
-        for (int e = 0; e < kSampleEach; ++e) {
-            const int i = tid * each + e;
+#pragma unroll 1
+        for (int i = i0; i < i1; ++i) {
+            const float l = sample_value((uint32_t)(list[i] >> 32));
             // the first of all always
-            if (e < each && i < count &&
-                ((lo == 0 && i == 0) ||
-                 ((!(set.p < 1.f) || run < target) && set.keeps(sw.weight(sample_value((uint32_t)(list[i] >> 32))))))) {
+            if ((lo == 0 && l == largest && i == 0) || ((double)run < rest && set.keeps(sw.weight(l)))) {
                 kept = i + 1;
-                atomicAdd((unsigned long long*)&sh.kept[of[e]], (unsigned long long)q[e]);   // whole numbers: in any order
+                const int of = slice_of(list[i]);
+                atomicAdd((unsigned long long*)&sh.kept[of], (unsigned long long)units_in(of, l));   // whole: in any order
             }
-            run += (double)q[e] * unit * sh.factor[of[e]];
+            run += sw.units(l);
         }
 #pragma unroll
         for (int m = 1; m < 64; m <<= 1) {
@@ -919,7 +984,9 @@ __device__ __forceinline__ bool sample_summed(const SampleArgs& a, int b, const 
     const int c0 = s * a.slice, c1 = c0 + a.slice < row.pieces ? c0 + a.slice : row.pieces;
     uint64_t upto_here = 0;
     for (int c = c0; c < c1; c += kSampleThreads) {
-        const uint4 v = sample_load(row, c + tid, c1);
+        uint4 loaded[1];
+        sample_load<DT, 1>(row, c + tid, 0, c1, loaded);
+        const uint4 v = loaded[0];
         const int i0 = (c + tid) * P - row.skew;
         uint64_t q[P], mine = 0, step;
         sample_values<DT>(v, [&](int e, float l) {
