@@ -12,10 +12,12 @@ namespace {
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 constexpr int64_t kFar = (int64_t)1 << 40;
+constexpr int64_t kMostRows = 1048560;
+static_assert(kMostRows / kLoraTile < 65535, "tiles fit a grid");
 
 bool sizes(const char* fn, int64_t T, int64_t K, int64_t N, int64_t R) {
-    // row tiles are the grid's second axis
-    if (T < 0 || T > (int64_t)65535 * kLoraRows || K < 8 || K >= (int64_t)1 << 24 || K % 8 != 0 || N < 0 || N >= (int64_t)1 << 24) {
+    // tiles of rows are the grid's second axis
+    if (T < 0 || T > kMostRows || K < 8 || K >= (int64_t)1 << 24 || K % 8 != 0 || N < 0 || N >= (int64_t)1 << 24) {
         fail(NVFP4_ERR_INVALID_ARG, "%s: T = %lld must be in [0, 1048560], K = %lld a multiple of 8 in [8, 2^24), N = %lld in [0, 2^24)",
              fn, (long long)T, (long long)K, (long long)N);
         return false;
@@ -27,41 +29,62 @@ bool sizes(const char* fn, int64_t T, int64_t K, int64_t N, int64_t R) {
     return true;
 }
 
-// Rows up to which each of a tile's adapters gets its own workgroups (their
-// grid's third axis); beyond, a workgroup takes them one after another.
-constexpr int64_t kLoraApart = 256;
-
 struct LoraShape {
-    int slices, slice, places;
+    int slices, slice, places, groups;   // groups: the grid's second axis
 };
 LoraShape lora_shape(int64_t T, int64_t K, int64_t L) {
     LoraShape s;
-    const int64_t tiles = (T + kLoraRows - 1) / kLoraRows;
-    s.places = T <= kLoraApart ? (int)(L < kLoraRows ? (L < 1 ? 1 : L) : kLoraRows) : 1;
-    // slices of at least a chunk for each wave, as many as make about 512 workgroups of tiles with all their places
-    int64_t want = (512 + tiles * s.places - 1) / (tiles * s.places);
-    if (want < 1) want = 1;
+    s.places = T <= kLoraLists ? (int)(L < T ? (L < 1 ? 1 : L) : T) : 0;
+    s.groups = s.places ? s.places : (int)((T + kLoraTile - 1) / kLoraTile);
+    // K slices of at least a chunk for each wave, as many as make about 512
+    // workgroups; k_lora_up reads them all for each of its column blocks (4099
+    // prompt rows, rank 32: 48.4 us in all with 4, 52 with 8, 53 with 2; 133 rows
+    // of 12 adapters, rank 64: 17.7 with 8, 19.8 with 4)
+    int64_t want = (512 + s.groups - 1) / s.groups;
     const int64_t most = (K + 511) / 512;
     if (want > most) want = most;
-    if (want > 16) want = 16;
+    if (want > (s.places ? 8 : 4)) want = s.places ? 8 : 4;
     s.slice = (int)round_up((K + want - 1) / want, 128);
     s.slices = (int)((K + s.slice - 1) / s.slice);
     return s;
 }
 
+// The grid's third axis.  Shares of a list, where adapters have few workgroups
+// otherwise: rows / 64 at most.  Tiles: two turns, so that where one prompt
+// ends and the next begins both adapters go at once.
+unsigned shares(int64_t T, int places, int64_t blocks) {
+    if (!places) return 2;
+    const int64_t want = 1024 / (blocks * places), most = (T + kLoraTile - 1) / kLoraTile;
+    return (unsigned)(want < 1 ? 1 : want < most ? want : most);
+}
+
+template <int RT, int MT, bool F16>
+void launch_down(const LoraArgs& a, const LoraShape& s, hipStream_t st) {
+    hipLaunchKernelGGL((k_lora_down<RT, MT, F16>), dim3((unsigned)a.slices, (unsigned)s.groups, shares(a.T, s.places, a.slices)),
+                       dim3(kLoraThreads), 0, st, a);
+}
+template <int KT, bool F16>
+void launch_up(LoraArgs a, const LoraShape& s, hipStream_t st) {
+    // as many columns a wave as leave 512 workgroups (tiles, whose rows are 64: 1024), up to 256
+    const int64_t enough = s.places ? 512 : 1024;
+    int64_t blocks;
+    a.cols = 8 * kLoraCols;
+    for (;; a.cols /= 2) {
+        blocks = (a.N + kLoraWaves * a.cols - 1) / (kLoraWaves * a.cols);
+        if (a.cols == kLoraCols || blocks * s.groups >= enough) break;
+    }
+    hipLaunchKernelGGL((k_lora_up<KT, F16>), dim3((unsigned)blocks, (unsigned)s.groups, shares(a.T, s.places, blocks)),
+                       dim3(kLoraThreads), 0, st, a);
+}
 template <bool F16>
 void launch(const LoraArgs& a, const LoraShape& s, hipStream_t st) {
-    const int tiles = (a.T + kLoraRows - 1) / kLoraRows;
-    const dim3 down((unsigned)a.slices, (unsigned)tiles, (unsigned)s.places), block(kLoraThreads);
-    const int per = kLoraWaves * kLoraCols;
-    const dim3 up((unsigned)((a.N + per - 1) / per), (unsigned)tiles, (unsigned)s.places);
-    if (a.R <= 16) hipLaunchKernelGGL((k_lora_down<1, F16>), down, block, 0, st, a);
-    else if (a.R <= 32) hipLaunchKernelGGL((k_lora_down<2, F16>), down, block, 0, st, a);
-    else if (a.R <= 64) hipLaunchKernelGGL((k_lora_down<4, F16>), down, block, 0, st, a);
-    else hipLaunchKernelGGL((k_lora_down<8, F16>), down, block, 0, st, a);
-    if (a.R <= 32) hipLaunchKernelGGL((k_lora_up<1, F16>), up, block, 0, st, a);
-    else if (a.R <= 64) hipLaunchKernelGGL((k_lora_up<2, F16>), up, block, 0, st, a);
-    else hipLaunchKernelGGL((k_lora_up<4, F16>), up, block, 0, st, a);
+    if (a.R <= 16) launch_down<1, 4, F16>(a, s, st);
+    else if (a.R <= 32) launch_down<2, 4, F16>(a, s, st);
+    else if (a.R <= 64) launch_down<4, 2, F16>(a, s, st);
+    else launch_down<8, 1, F16>(a, s, st);
+    if (a.R <= 32) launch_up<1, F16>(a, s, st);
+    else if (a.R <= 64) launch_up<2, F16>(a, s, st);
+    else launch_up<4, F16>(a, s, st);
 }
 
 }  // namespace
@@ -70,7 +93,7 @@ extern "C" {
 
 int64_t nvfp4_lora_workspace_bytes(int64_t T, int64_t K, int64_t N, int64_t R) {
     if (!sizes("nvfp4_lora_workspace_bytes", T, K, N, R)) return -1;
-    // the most slices that any number of adapters gives
+    // one adapter has the most slices
     return T == 0 || N == 0 ? 0 : (int64_t)lora_shape(T, K, 1).slices * T * R * 4;
 }
 
@@ -121,6 +144,7 @@ nvfp4_status nvfp4_lora_add(const void* x, int64_t ld_x, const void* a, int64_t 
     g.L = (int)L;
     g.slices = s.slices;
     g.slice = s.slice;
+    g.places = s.places;
     g.vec = aligned(y, 16) && aligned(out, 16) && ld_y % 8 == 0 && ld_o % 8 == 0;
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (f16) launch<true>(g, s, st);
