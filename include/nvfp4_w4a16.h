@@ -668,7 +668,7 @@ nvfp4_status nvfp4_paged_attention(const nvfp4_kv_cache* cache, const void* q, i
  *   captured step advances by itself; no other overlap.
  *   workspace: nvfp4_kv_plan_workspace_bytes(B, T) bytes (0 for small calls), 8-byte
  *   aligned, any contents.
- * Errors: sizes (B, T, max_pages * page_size < 2^30, F < 2^31, ld_table), NULL
+ * Errors: sizes (B, T, max_pages * page_size and F < 2^30, ld_table), NULL
  * pointers -> INVALID_ARG; misaligned -> ALIGNMENT; workspace too small ->
  * BUFFER_TOO_SMALL. */
 int64_t nvfp4_kv_plan_workspace_bytes(int64_t B, int64_t T); /* < 0 if invalid */

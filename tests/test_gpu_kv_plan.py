@@ -78,6 +78,17 @@ def test_pages_without_a_slot():
     check(np.array([0, 17]), np.array([70, 20]), np.array([[0] * 6, [-1, 2 ** 31 - 1] + [0] * 4]), free, 0, 16, 90)
 
 
+@pytest.mark.parametrize("B", [5, 300, 5000])
+def test_lengths_beyond_all_limits(B):
+    """Sums of lengths past 32 bits, and lengths whose own sum is: those requests are refused, the ones before them not."""
+    cached, new = np.full(B, 20), np.full(B, 3)
+    new[1::2] = 2 ** 31 - 1
+    cached[2::4] = 2 ** 31 - 1
+    check(cached, new, np.zeros((B, 4)), np.arange(4 * B), 0, 16, 50)
+    new[:] = 2 ** 30
+    check(cached, new, np.zeros((B, 4)), np.arange(4 * B), 0, 16, 50)
+
+
 @pytest.mark.parametrize("tokens", [0, 5, 5000])
 def test_no_requests_and_no_rows(tokens):
     got = check(np.zeros(0), np.zeros(0), np.zeros((0, 4)), np.arange(3), 1, 16, tokens)

@@ -41,7 +41,7 @@ def last():
 @pytest.mark.parametrize("kw,status,needle", [
     (dict(B=-1), INVALID, "B ="), (dict(B=1 << 30), INVALID, "B ="), (dict(T=-1), INVALID, "T ="), (dict(T=1 << 30), INVALID, "T ="),
     (dict(page=0), INVALID, "page_size"), (dict(mp=-1), INVALID, "max_pages"), (dict(mp=1 << 26, ld=1 << 26), INVALID, "2^30"),
-    (dict(ld=7), INVALID, "ld_table"), (dict(F=-1), INVALID, "free"), (dict(F=1 << 31), INVALID, "free"),
+    (dict(ld=7), INVALID, "ld_table"), (dict(F=-1), INVALID, "free"), (dict(F=1 << 30), INVALID, "free"),
     (dict(head=None), INVALID, "NULL"), (dict(cached=None), INVALID, "NULL"), (dict(new=None), INVALID, "NULL"),
     (dict(table=None), INVALID, "NULL"), (dict(free=None), INVALID, "NULL"), (dict(slots=None), INVALID, "NULL"),
     (dict(lengths=None), INVALID, "NULL"), (dict(offsets=None), INVALID, "NULL"), (dict(out=None), INVALID, "NULL"),

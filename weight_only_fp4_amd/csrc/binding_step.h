@@ -17,11 +17,22 @@ at::Tensor workspace_of(PyObject* o, int64_t need, int64_t zeros, c10::Device de
 const int32_t* ints(const at::Tensor& t) { return static_cast<const int32_t*>(t.data_ptr()); }
 int32_t* ints_out(const at::Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); }
 
-// kv_plan(cached, new, page_table, free_pages, head, page_size, tokens, out, workspace)
+// `n` values of `base` from place `from` on, which it moves past them and the
+// rest of 16 bytes: a small call's outputs are one allocation (six cost 4 us).
+at::Tensor part_of(const at::Tensor& base, int64_t& from, int64_t n) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(base.storage()), base.key_set(), base.dtype());
+    c10::TensorImpl* impl = t.unsafeGetTensorImpl();
+    impl->set_storage_offset(from);
+    impl->set_sizes_contiguous({n});
+    from += (n + 3) / 4 * 4;
+    return t;
+}
+
+// kv_plan(cached, new, page_table, free_pages, head, page_size, tokens, out)
 // -> (slots, positions, requests, lengths, offsets, head)
 PyObject* kv_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    arguments(n, 9);
+    arguments(n, 8);
     const at::Tensor& cached = tensor(a[0], "cached");
     TORCH_CHECK_VALUE(cached.scalar_type() == at::kInt && cached.dim() == 1 && cached.is_cuda(),
                       "cached must be a 1-d int32 tensor on the GPU");
@@ -48,13 +59,22 @@ PyObject* kv_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     const char* names[6] = {"slots", "positions", "requests", "lengths", "offsets", "head"};
     const int64_t sizes[6] = {T, T, T, B, B + 1, 1};
-    at::Tensor out[6];
-    for (int i = 0; i < 6; ++i) out[i] = output(given[i], names[i], at::kInt, {sizes[i]}, dev);
     const int64_t need = nvfp4_kv_plan_workspace_bytes(B, T);
-    at::Tensor ws = workspace_of(a[8], need, 0, dev);
+    if (need < 0) check(NVFP4_ERR_INVALID_ARG);
+    at::Tensor out[6], ws;
+    if (a[7] == Py_None) {
+        int64_t total = need / 4, from = 0;
+        for (int64_t n : sizes) total += (n + 3) / 4 * 4;
+        const at::Tensor all = fresh({total}, at::kInt, dev);
+        for (int i = 0; i < 6; ++i) out[i] = part_of(all, from, sizes[i]);
+        ws = part_of(all, from, need / 4);
+    } else {
+        for (int i = 0; i < 6; ++i) out[i] = output(given[i], names[i], at::kInt, {sizes[i]}, dev);
+        ws = workspace_of(Py_None, need, 0, dev);
+    }
     check(nvfp4_kv_plan(ints(cached), ints(fresh_tokens), B, ints_out(table), leading(table), table.size(1), page, ints(list),
                         list.size(0), ints(head), T, ints_out(out[0]), ints_out(out[1]), ints_out(out[2]), ints_out(out[3]),
-                        ints_out(out[4]), ints_out(out[5]), ws.data_ptr(), (int64_t)ws.nbytes(), stream_of(dev)));
+                        ints_out(out[4]), ints_out(out[5]), ws.data_ptr(), need, stream_of(dev)));
     PyObject* t = PyTuple_New(6);
     if (!t) throw python_error();
     for (int i = 0; i < 6; ++i) PyTuple_SET_ITEM(t, i, THPVariable_Wrap(std::move(out[i])));

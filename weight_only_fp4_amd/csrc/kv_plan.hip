@@ -13,10 +13,19 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 constexpr int64_t kMost = (int64_t)1 << 30;   // requests, rows and tokens of a table's row stay below
 
-// Rows written by the scans' own workgroup.
-constexpr int64_t kPlanOneLaunch = 4096;
+// Rows that one workgroup writes alone where an output is an input's memory.
+constexpr int64_t kPlanAlone = 4096;
 
-bool one_launch(int64_t B, int64_t T) { return B <= kPlanLds && T <= kPlanOneLaunch; }
+// Whether the call may take two launches, by its sizes alone (the workspace
+// is for them).
+bool may_share(int64_t B, int64_t T) { return B > kPlanLds || T > kPlanAlone; }
+
+template <int THREADS>
+void launch_whole(const PlanArgs& a, bool alone, hipStream_t st) {
+    // two rows a thread: half as many scans as with one
+    const int64_t groups = ((int64_t)a.T + 2 * THREADS - 1) / (2 * THREADS);
+    hipLaunchKernelGGL((k_plan<THREADS, true>), dim3(alone || groups < 1 ? 1u : (unsigned)groups), dim3(THREADS), 0, st, a);
+}
 
 }  // namespace
 
@@ -27,7 +36,7 @@ int64_t nvfp4_kv_plan_workspace_bytes(int64_t B, int64_t T) {
         fail(NVFP4_ERR_INVALID_ARG, "nvfp4_kv_plan_workspace_bytes: B = %lld, T = %lld", (long long)B, (long long)T);
         return -1;
     }
-    return one_launch(B, T) ? 0 : B * (int64_t)sizeof(int2);
+    return may_share(B, T) ? B * (int64_t)sizeof(int2) : 0;
 }
 
 nvfp4_status nvfp4_kv_plan(const int32_t* cached, const int32_t* fresh, int64_t B, int32_t* page_table, int64_t ld_table,
@@ -43,7 +52,7 @@ nvfp4_status nvfp4_kv_plan(const int32_t* cached, const int32_t* fresh, int64_t 
     if (ld_table < max_pages || ld_table >= (int64_t)1 << 40)
         return fail(NVFP4_ERR_INVALID_ARG, "%s: ld_table = %lld < max_pages = %lld or too large", fn, (long long)ld_table,
                     (long long)max_pages);
-    if (F < 0 || F >= (int64_t)1 << 31) return fail(NVFP4_ERR_INVALID_ARG, "%s: F = %lld free pages", fn, (long long)F);
+    if (F < 0 || F >= kMost) return fail(NVFP4_ERR_INVALID_ARG, "%s: F = %lld free pages", fn, (long long)F);
     if (!head || !head_out || !offsets || (F > 0 && !free_pages) || (B > 0 && (!cached || !fresh || !lengths)) ||
         (B > 0 && max_pages > 0 && !page_table) || (T > 0 && (!slots || !positions || !requests)))
         return fail(NVFP4_ERR_INVALID_ARG, "%s: NULL pointer", fn);
@@ -77,15 +86,26 @@ nvfp4_status nvfp4_kv_plan(const int32_t* cached, const int32_t* fresh, int64_t 
     a.width = (int)max_pages;
     a.page = (int)page_size;
     a.T = (int)T;
+    // umulhi(t, ceil(2^(32 + s) / page_size)) >> s is t / page_size for t < 2^31 with 2^s < page_size <= 2^(s + 1)
+    a.page_shift = 0;
+    while ((int64_t)2 << a.page_shift < page_size) ++a.page_shift;
+    a.page_magic = page_size == 1 ? 0u
+                   : (uint32_t)((((uint64_t)1 << (32 + a.page_shift)) + (uint64_t)page_size - 1) / (uint64_t)page_size);
     hipStream_t st = static_cast<hipStream_t>(stream);
-    if (one_launch(B, T)) {
-        hipLaunchKernelGGL((k_plan<true>), dim3(1), dim3(kPlanThreads), 0, st, a);
+    const bool in_place = lengths == cached || head_out == head;
+    if (B <= kPlanLds && (!in_place || T <= kPlanAlone)) {
+        // few requests: fewer waves to wait for at each barrier
+        if (B <= 64 * kPlanItems && T <= 256) launch_whole<64>(a, in_place, st);
+        else if (B <= 256 * kPlanItems) launch_whole<256>(a, in_place, st);
+        else launch_whole<kPlanMaxThreads>(a, in_place, st);
         return launched(fn);
     }
-    hipLaunchKernelGGL((k_plan<false>), dim3(1), dim3(kPlanThreads), 0, st, a);
-    nvfp4_status s = launched(fn);
+    // offsets and the workspace are written here, for the rows' launch
+    if (B <= 256 * kPlanItems) hipLaunchKernelGGL((k_plan<256, false>), dim3(1), dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((k_plan<kPlanMaxThreads, false>), dim3(1), dim3(kPlanMaxThreads), 0, st, a);
+    const nvfp4_status s = launched(fn);
     if (s != NVFP4_OK || T == 0) return s;
-    hipLaunchKernelGGL(k_plan_rows, dim3((unsigned)((T + kPlanRows - 1) / kPlanRows)), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(k_plan_rows, dim3((unsigned)((T + kPlanRows - 1) / kPlanRows)), dim3(kPlanRows), 0, st, a);
     return launched(fn);
 }
 

@@ -46,7 +46,7 @@ def kv_plan(cached, new, page_table, free_pages, free_head, page_size, tokens, o
     ``paged_attention``.  A request whose pages or rows do not fit gets no page and no slots, and keeps its cached length.
     out: a KvPlan (or six tensors) to write to, whose lengths may be cached itself and its head free_head."""
     return KvPlan(*(_attention._binding or _attention._native()).kv_plan(cached, new, page_table, free_pages, free_head,
-                                                                         page_size, tokens, out, None))
+                                                                         page_size, tokens, out))
 
 
 # ------------------------------------------------------------------- lora --
