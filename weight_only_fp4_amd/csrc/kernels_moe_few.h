@@ -14,14 +14,13 @@
 // bounds them is HBM, behind a chain of latencies (ids, rows, weights).
 //
 // There is no routing launch.  k_moe_few_fc1 has a grid row per pair, and the
-// workgroups of the first pair of an expert do all of the expert's pairs; its
-// first column also writes each pair's group (the first pair of its expert),
-// its place in it and the groups' sizes.  k_moe_few_fc2 makes a list of (expert,
-// up to 4 MG rows) from them; a workgroup owns 16 columns of out and a share of
-// that list's K chunks, cut evenly into one stretch per wave, which a wave's
-// ring of loads streams without a stop where an expert ends.  So the sum over a
-// token's experts needs no exchange of rows: it is formed where the products
-// are, and split workgroups exchange 16 columns of T rows.
+// workgroups of the first pair of an expert do all of the expert's pairs.  One
+// more workgroup makes the second kernel's list meanwhile: items of an expert
+// and up to 4 MG of its pairs.  A workgroup of k_moe_few_fc2 owns 16 columns of
+// out and a share of the items' K chunks, cut evenly into one stretch per wave,
+// which a wave's ring of loads streams without a stop where an expert ends.  So
+// the sum over a token's experts needs no exchange of rows: it is formed where
+// the products are, and split workgroups exchange 16 columns of T rows.
 //
 // Waves add into accumulators of their own and are summed in a fixed order, as
 // the splits are: no result depends on timing.
@@ -35,6 +34,18 @@ constexpr int kFewPairs = 512;
 constexpr int kFewWaves = 4;           // of a workgroup of k_moe_few_fc2
 constexpr int kFewDepth = 4;           // ring of loads
 
+// Up to 4 MG pairs of one expert: places first .. first + rows - 1 of the list.
+struct FewItem {
+    int32_t e, first, rows;
+    float g;   // the expert's global scale
+};
+struct FewList {
+    int32_t items, reserved[3];
+    FewItem item[kFewPairs];
+    int32_t pair[kFewPairs];      // pairs by expert, in the order of the experts' first ones
+    float weight[kFewPairs];
+};
+
 struct FewArgs {
     const uint16_t* x;
     int64_t ld_x;
@@ -46,9 +57,7 @@ struct FewArgs {
     const uint16_t* pre1;
     const uint16_t* pre2;
     uint16_t* a;          // [P][ld_a] workspace
-    int32_t* group;       // [P]: first pair of the pair's expert, -1 if it has none
-    int32_t* place;       // [P]: the pair's place among that expert's pairs
-    int32_t* size;        // [P]: the expert's pairs at its first, 0 elsewhere
+    FewList* list;        // workspace
     uint16_t* out;
     int64_t ld_a, ld_o;
     SplitK sk;            // k_moe_few_fc2's splits: partials [S][units][T * 16], counters [units]
@@ -57,7 +66,66 @@ struct FewArgs {
     int NU1, KC1, NU2, KC2;
 };
 
-// Grid: (units of W1 / NT, pairs).  NT = 2 with the gate (a pair of units: gate, up).
+// The second kernel's list, by one workgroup: a pair's place is that of its
+// expert's first pair, plus the pairs of the expert before it.
+template <int MG, int THREADS>
+__device__ __forceinline__ void few_list(const FewArgs& f, int32_t* ids, int32_t* place) {
+    __shared__ int32_t s_sums[THREADS / 64][2];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    for (int p = tid; p < f.P; p += THREADS) ids[p] = f.ids[p];
+    __syncthreads();
+    int rows = 0, items = 0;   // of the rounds before
+    for (int p0 = 0; p0 < f.P; p0 += THREADS) {
+        const int p = p0 + tid, e = p < f.P ? ids[p] : -1;
+        const bool valid = e >= 0 && e < f.E;
+        int before = 0, all = 0;
+        if (valid)
+            for (int q = 0; q < f.P; ++q) {
+                const bool same = ids[q] == e;
+                all += same;
+                before += same && q < p;
+            }
+        const bool first = valid && before == 0;
+        const int n = first ? all : 0, its = (n + 4 * MG - 1) / (4 * MG);
+        int a = n, b = its;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int oa = __shfl_up(a, d), ob = __shfl_up(b, d);
+            if (lane >= d) a += oa, b += ob;
+        }
+        if (lane == 63) s_sums[w][0] = a, s_sums[w][1] = b;
+        __syncthreads();
+        int ra = rows, rb = items;
+#pragma unroll
+        for (int i = 0; i < THREADS / 64; ++i) {
+            if (i < w) ra += s_sums[i][0], rb += s_sums[i][1];
+            rows += s_sums[i][0];
+            items += s_sums[i][1];
+        }
+        ra += a - n;
+        rb += b - its;
+        if (first) {
+            place[p] = ra;
+            const float g = global_scale_at(f.g2, e, f.g_div);
+            for (int i = 0; i < its; ++i)
+                f.list->item[rb + i] = FewItem{e, ra + 4 * MG * i, n - 4 * MG * i < 4 * MG ? n - 4 * MG * i : 4 * MG, g};
+        }
+        __syncthreads();
+    }
+    for (int p = tid; p < f.P; p += THREADS) {
+        const int e = ids[p];
+        if (e < 0 || e >= f.E) continue;
+        int before = 0, q = 0;
+        while (ids[q] != e) ++q;   // ends at p
+        const int first = q;
+        for (; q < p; ++q) before += ids[q] == e;
+        f.list->pair[place[first] + before] = p;
+        f.list->weight[place[first] + before] = f.weights[p];
+    }
+    if (tid == 0) f.list->items = items;
+}
+
+// Grid: (units of W1 / NT, pairs + 1).  NT = 2 with the gate (a pair of units: gate, up).
 template <int MG, int W, bool F16, bool PRE, int ACT>
 __global__ void __launch_bounds__(W * 64) k_moe_few_fc1(FewArgs f) {
     constexpr int NT = ACT == kActSiluGlu ? 2 : 1;
@@ -68,20 +136,20 @@ __global__ void __launch_bounds__(W * 64) k_moe_few_fc1(FewArgs f) {
     __shared__ int32_t pairs[kFewPairs];
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int p = blockIdx.y, u0 = blockIdx.x * NT;
+    const int p = (int)blockIdx.y - 1, u0 = blockIdx.x * NT;
+    if (p < 0) {   // first in the grid: it is not what the launch waits for in the end
+        if (blockIdx.x == 0) few_list<MG, W * 64>(f, tokens, pairs);
+        return;
+    }
     const int e = f.ids[p];
-    const bool none = e < 0 || e >= f.E;
+    if (e < 0 || e >= f.E) return;
     // the expert's pairs, in order (every wave makes the same list)
     int count = 0;
-    bool first = true;
     for (int q0 = 0; q0 < f.P; q0 += 64) {
         const int q = q0 + lane;
         const bool same = q < f.P && f.ids[q] == e;
         const uint64_t m = __ballot(same);
-        if (q0 <= p) {
-            const uint64_t before = q0 + 64 <= p ? ~0ull : ((1ull << (p - q0)) - 1);
-            if (m & before) first = false;
-        }
+        if (q0 <= p && (m & (q0 + 64 <= p ? ~0ull : (1ull << (p - q0)) - 1))) return;   // not its first
         if (same) {
             const int at = count + __popcll(m & ((1ull << lane) - 1));
             pairs[at] = q;
@@ -89,16 +157,6 @@ __global__ void __launch_bounds__(W * 64) k_moe_few_fc1(FewArgs f) {
         }
         count += __popcll(m);
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-        f.size[p] = first && !none ? count : 0;
-        if (none) f.group[p] = -1;
-    }
-    if (none || !first) return;
-    if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i < count; i += W * 64) {
-            f.group[pairs[i]] = p;
-            f.place[pairs[i]] = i;
-        }
     const int c0 = f.KC1 * w / W, c1 = f.KC1 * (w + 1) / W;
     const int64_t blk0 = f.w1.block(e, u0, 0);
     const WaveWeights ww{f.w1.codes + blk0 * kCodeBlock, f.w1.scales + blk0 * kScaleBlock,
@@ -136,13 +194,9 @@ __global__ void __launch_bounds__(W * 64) k_moe_few_fc1(FewArgs f) {
 
 struct FewShared {
     float2 lut[256];
-    int32_t pair[kFewPairs];      // pairs by group
+    FewItem item[kFewPairs];
+    int32_t pair[kFewPairs];
     float weight[kFewPairs];
-    int32_t item_e[kFewPairs];    // items: up to 4 MG rows of an expert
-    int32_t item_first[kFewPairs];
-    int32_t item_rows[kFewPairs];
-    float item_g[kFewPairs];
-    int32_t sums[kFewWaves][2];
     int flag;
 };
 
@@ -157,71 +211,14 @@ __global__ void __launch_bounds__(kFewWaves * 64) k_moe_few_fc2(FewArgs f) {
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int u = blockIdx.x, S = f.sk.S, s = blockIdx.y;
     const int out_n = f.T * 16;
+    const int items = f.list->items;
+    for (int i = tid; i < f.P; i += kThreads) {   // (what is past the items and their pairs is not read)
+        sh.item[i] = f.list->item[i];
+        sh.pair[i] = f.list->pair[i];
+        sh.weight[i] = f.list->weight[i];
+    }
     build_scale_table(sh.lut, f.w2.mx);
     for (int i = tid; i < kFewWaves * out_n; i += kThreads) sums[i] = 0.f;
-    // lists from the groups: thread tid scans pairs tid and tid + 256 by their order
-    constexpr int kEach = kFewPairs / kThreads;
-    int base_rows = 0, items = 0;
-    int first_row[kEach], n_rows[kEach];
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-        const int p = j * kThreads + tid;
-        const int n = p < f.P ? f.size[p] : 0, its = (n + 4 * MG - 1) / (4 * MG);
-        int a = n, b = its;   // inclusive scans of rows and items
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int oa = __shfl_up(a, d), ob = __shfl_up(b, d);
-            if (lane >= d) a += oa, b += ob;
-        }
-        __syncthreads();
-        if (lane == 63) sh.sums[w][0] = a, sh.sums[w][1] = b;
-        __syncthreads();
-        int ra = base_rows, rb = items;
-#pragma unroll
-        for (int i = 0; i < kFewWaves; ++i) {
-            if (i < w) ra += sh.sums[i][0], rb += sh.sums[i][1];
-            base_rows += sh.sums[i][0];
-            items += sh.sums[i][1];
-        }
-        first_row[j] = ra + a - n;
-        n_rows[j] = n;
-        if (n > 0) {
-            const int e = f.ids[p];
-            const float g = global_scale_at(f.g2, e, f.g_div);
-            for (int i = 0; i < its; ++i) {
-                const int at = rb + b - its + i;
-                sh.item_e[at] = e;
-                sh.item_first[at] = first_row[j] + 4 * MG * i;
-                sh.item_rows[at] = n - 4 * MG * i < 4 * MG ? n - 4 * MG * i : 4 * MG;
-                sh.item_g[at] = g;
-            }
-        }
-    }
-    // the place of a group's rows, kept where its first pair's weight will not be needed: in weight[]
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-        const int p = j * kThreads + tid;
-        if (p < f.P && n_rows[j] > 0) sh.weight[p] = __int_as_float(first_row[j]);
-    }
-    __syncthreads();
-    int at[kEach];
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-        const int p = j * kThreads + tid;
-        at[j] = -1;
-        if (p < f.P) {
-            const int g = f.group[p];
-            if (g >= 0) at[j] = __float_as_int(sh.weight[g]) + f.place[p];
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kEach; ++j)
-        if (at[j] >= 0) {
-            const int p = j * kThreads + tid;
-            sh.pair[at[j]] = p;
-            sh.weight[at[j]] = f.weights[p];
-        }
     __syncthreads();
 
     // this wave's stretch of all chunks
@@ -238,8 +235,8 @@ __global__ void __launch_bounds__(kFewWaves * 64) k_moe_few_fc2(FewArgs f) {
         const uint8_t *codes = nullptr, *scales = nullptr;   // the load side's unit
         uint32_t row[MG];
         auto enter = [&]() {   // the load side's item
-            const int e = __builtin_amdgcn_readfirstlane(sh.item_e[ld.item]);
-            const int first = sh.item_first[ld.item], rows = sh.item_rows[ld.item];
+            const int e = __builtin_amdgcn_readfirstlane(sh.item[ld.item].e);
+            const int first = sh.item[ld.item].first, rows = sh.item[ld.item].rows;
             const int64_t blk = f.w2.block(e, u, 0);
             codes = f.w2.codes + blk * kCodeBlock;
             scales = f.w2.scales + blk * kScaleBlock;
@@ -280,8 +277,8 @@ __global__ void __launch_bounds__(kFewWaves * 64) k_moe_few_fc2(FewArgs f) {
             const bool ends = us.chunk == f.KC2 - 1;
             if (ends || i == n - 1) {
                 // the item's rows into the tokens' sums: lane l < 16 has column l
-                const int first = sh.item_first[us.item], rows = sh.item_rows[us.item];
-                const float gv = sh.item_g[us.item];
+                const int first = sh.item[us.item].first, rows = sh.item[us.item].rows;
+                const float gv = sh.item[us.item].g;
 #pragma unroll
                 for (int mg = 0; mg < MG; ++mg)
 #pragma unroll

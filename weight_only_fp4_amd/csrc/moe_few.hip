@@ -16,7 +16,7 @@ constexpr int64_t kFewLd = (int64_t)1 << 22;                          // offsets
 
 struct FewShape {
     int mg, S;
-    int64_t a_at, pairs_at, part_at, total;   // workspace: counters, a, the pairs' lists, partial sums
+    int64_t a_at, list_at, part_at, total;   // workspace: counters, a, FC2's list, partial sums
 };
 
 FewShape few_shape(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
@@ -31,8 +31,8 @@ FewShape few_shape(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
     if (S > 16) S = 16;
     s.S = S < 1 ? 1 : (int)S;
     s.a_at = NVFP4_MOE_LAYER_COUNTER_BYTES;
-    s.pairs_at = s.a_at + round_up(P * I * 2, 256);
-    s.part_at = s.pairs_at + round_up(3 * P * 4, 256);
+    s.list_at = s.a_at + round_up(P * I * 2, 256);
+    s.part_at = s.list_at + round_up((int64_t)sizeof(FewList), 256);
     s.total = s.part_at + (s.S > 1 ? (int64_t)s.S * NU * T * kUnitN * 4 : 0);
     return s;
 }
@@ -54,7 +54,7 @@ nvfp4_status sizes(const char* fn, int64_t T, int64_t k, int64_t E, int64_t H, i
 template <int MG, bool F16, bool PRE, int ACT>
 void launch_fc1(const FewArgs& f, hipStream_t st) {
     constexpr int NT = ACT == kActSiluGlu ? 2 : 1;
-    hipLaunchKernelGGL((k_moe_few_fc1<MG, 4, F16, PRE, ACT>), dim3((unsigned)((f.NU1 + NT - 1) / NT), (unsigned)f.P),
+    hipLaunchKernelGGL((k_moe_few_fc1<MG, 4, F16, PRE, ACT>), dim3((unsigned)((f.NU1 + NT - 1) / NT), (unsigned)f.P + 1),
                        dim3(256), 0, st, f);
 }
 template <int MG, bool F16, bool PRE>
@@ -133,9 +133,7 @@ nvfp4_status nvfp4_moe_layer(const void* x, int64_t ld_x, const int32_t* topk_id
     char* ws = static_cast<char*>(workspace);
     f.a = reinterpret_cast<uint16_t*>(ws + sh.a_at);
     f.P = (int)(T * k);
-    f.group = reinterpret_cast<int32_t*>(ws + sh.pairs_at);
-    f.place = f.group + f.P;
-    f.size = f.place + f.P;
+    f.list = reinterpret_cast<FewList*>(ws + sh.list_at);
     f.out = static_cast<uint16_t*>(out);
     f.ld_a = I;
     f.ld_o = ld_o;
