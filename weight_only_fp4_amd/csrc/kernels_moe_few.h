@@ -13,9 +13,10 @@
 // each active expert's weights once while it has at most 4 MG rows.  What
 // bounds them is HBM, behind a chain of latencies (ids, rows, weights).
 //
-// There is no routing launch.  k_moe_few_fc1 has a grid row per pair, and the
-// workgroups of the first pair of an expert do all of the expert's pairs.  One
-// more workgroup makes the second kernel's list meanwhile: items of an expert
+// There is no routing launch.  k_moe_few_fc1 has a grid row per pair, and every
+// (4 MG)th pair of an expert has workgroups, which do it and those after it up
+// to the next.  (With an expert's pairs in one workgroup, one pass after another,
+// the busiest expert decides.)  One more workgroup makes the second kernel's list meanwhile: items of an expert
 // and up to 4 MG of its pairs.  A workgroup of k_moe_few_fc2 owns 16 columns of
 // out and a share of the items' K chunks, cut evenly into one stretch per wave,
 // which a wave's ring of loads streams without a stop where an expert ends.  So
@@ -31,8 +32,15 @@ namespace nvfp4 {
 
 constexpr int kFewTokens = 64;
 constexpr int kFewPairs = 512;
-constexpr int kFewWaves = 4;           // of a workgroup of k_moe_few_fc2
-constexpr int kFewDepth = 4;           // ring of loads
+// Shapes (us of the layer in a graph: 1 token of 128 experts, top-8, 2048 x 768;
+// 16 tokens of it; 5 tokens of 8 experts, top-2, 4096 x 14336):
+//   FC1, waves and depth of their rings: 4 and 2 13.6 / 40.8 / 89.1; 4 and 4 13.7
+//   / 44.2 / 90.5; 2 and 4 14.8 / 41.5 / 87.4; 1 and 4 15.5 / 43.2 / 87.0; 8 and 2
+//   13.8 / 49.0 / 93.2;
+//   FC2 (with 2 and 4 for FC1): 8 and 4 14.8 / 41.5 / 87.4; 8 and 2 14.2 / 42.1 /
+//   87.6; 4 and 4 14.7 / 42.7 / 88.1; 16 and 2 13.0 / 44.8 / 90.2.
+constexpr int kFewWaves1 = 4, kFewDepth1 = 2;
+constexpr int kFewWaves = 8, kFewDepth = 4;
 
 // Up to 4 MG pairs of one expert: places first .. first + rows - 1 of the list.
 struct FewItem {
@@ -126,13 +134,14 @@ __device__ __forceinline__ void few_list(const FewArgs& f, int32_t* ids, int32_t
 }
 
 // Grid: (units of W1 / NT, pairs + 1).  NT = 2 with the gate (a pair of units: gate, up).
-template <int MG, int W, bool F16, bool PRE, int ACT>
-__global__ void __launch_bounds__(W * 64) k_moe_few_fc1(FewArgs f) {
+template <int MG, bool F16, bool PRE, int ACT>
+__global__ void __launch_bounds__(kFewWaves1 * 64) k_moe_few_fc1(FewArgs f) {
+    constexpr int W = kFewWaves1;
     constexpr int NT = ACT == kActSiluGlu ? 2 : 1;
     constexpr int RLD = NT * 16;
     __shared__ float red[W][4 * MG * RLD];
     __shared__ float2 lut[256];
-    __shared__ int32_t tokens[kFewPairs];
+    __shared__ int32_t tokens[kFewPairs];   // (few_list's first)
     __shared__ int32_t pairs[kFewPairs];
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -143,52 +152,49 @@ __global__ void __launch_bounds__(W * 64) k_moe_few_fc1(FewArgs f) {
     }
     const int e = f.ids[p];
     if (e < 0 || e >= f.E) return;
-    // the expert's pairs, in order (every wave makes the same list)
-    int count = 0;
+    // the pair's place among its expert's pairs, and the pairs from it on (every
+    // wave makes the same list)
+    int place = 0, upto = 0;
     for (int q0 = 0; q0 < f.P; q0 += 64) {
         const int q = q0 + lane;
-        const bool same = q < f.P && f.ids[q] == e;
-        const uint64_t m = __ballot(same);
-        if (q0 <= p && (m & (q0 + 64 <= p ? ~0ull : (1ull << (p - q0)) - 1))) return;   // not its first
-        if (same) {
-            const int at = count + __popcll(m & ((1ull << lane) - 1));
-            pairs[at] = q;
-            tokens[at] = q / f.k;
+        const uint64_t same = __ballot(q < f.P && f.ids[q] == e);
+        if (q0 <= p) place += __popcll(same & (q0 + 64 <= p ? ~0ull : (1ull << (p - q0)) - 1));
+        if (q0 + 64 > p && (same >> lane) & 1ull) {
+            const int at = upto + __popcll(same & ((1ull << lane) - 1)) - place;
+            if (at >= 0 && at < 4 * MG) {
+                pairs[at] = q;
+                tokens[at] = q / f.k;
+            }
         }
-        count += __popcll(m);
+        upto += __popcll(same);
     }
+    if (place % (4 * MG) != 0) return;
+    const int rows = upto - place < 4 * MG ? upto - place : 4 * MG;
     const int c0 = f.KC1 * w / W, c1 = f.KC1 * (w + 1) / W;
     const int64_t blk0 = f.w1.block(e, u0, 0);
     const WaveWeights ww{f.w1.codes + blk0 * kCodeBlock, f.w1.scales + blk0 * kScaleBlock,
                          f.w1.unit_stride * kCodeBlock, f.w1.chunk_stride * kCodeBlock,
                          (f.NU1 - u0) < NT ? (f.NU1 - u0) : NT};
-    bool built = false;
     auto mid = [&]() {
-        if (built) return;
         build_scale_table(lut, f.w1.mx);
         wait_lgkmcnt0();   // only LDS writes need to be seen (the ring's loads stay in flight)
         asm volatile("s_barrier" ::: "memory");
-        built = true;
     };
     const float gv = global_scale_at(f.g1, e, f.g_div);
-    for (int r0 = 0; r0 < count; r0 += 4 * MG) {
-        const int rows = count - r0 < 4 * MG ? count - r0 : 4 * MG;
-        small_m_pass<MG, NT, kFewDepth, false, F16, PRE>(f.x, f.ld_x, rows, f.pre1, ww, c0, c1, f.H, lut, red[w], RLD,
-                                                         lane, mid, tokens + r0);
-        __syncthreads();
-        for (int t = threadIdx.x; t < rows * 16; t += W * 64) {
-            const int r = t >> 4, c = t & 15;
-            float s0 = 0.f, s1 = 0.f;
+    small_m_pass<MG, NT, kFewDepth1, false, F16, PRE>(f.x, f.ld_x, rows, f.pre1, ww, c0, c1, f.H, lut, red[w], RLD, lane,
+                                                     mid, tokens);
+    __syncthreads();
+    for (int t = threadIdx.x; t < rows * 16; t += W * 64) {
+        const int r = t >> 4, c = t & 15;
+        float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-            for (int wi = 0; wi < W; ++wi) {
-                s0 += red[wi][r * RLD + c];
-                if (NT == 2) s1 += red[wi][r * RLD + (NT - 1) * 16 + c];
-            }
-            const int n = (int)blockIdx.x * 16 + c;
-            const float v = ACT == kActSiluGlu ? silu_times(gv * s0, gv * s1) : relu_squared(gv * s0);
-            if (n < f.I) f.a[(int64_t)pairs[r0 + r] * f.ld_a + n] = (uint16_t)round_out<F16>(v);
+        for (int wi = 0; wi < W; ++wi) {
+            s0 += red[wi][r * RLD + c];
+            if (NT == 2) s1 += red[wi][r * RLD + (NT - 1) * 16 + c];
         }
-        __syncthreads();
+        const int n = (int)blockIdx.x * 16 + c;
+        const float v = ACT == kActSiluGlu ? silu_times(gv * s0, gv * s1) : relu_squared(gv * s0);
+        if (n < f.I) f.a[(int64_t)pairs[r] * f.ld_a + n] = (uint16_t)round_out<F16>(v);
     }
 }
 

@@ -23,7 +23,9 @@ FewShape few_shape(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
     FewShape s;
     const int64_t P = T * k, NU = (H + kUnitN - 1) / kUnitN, KC = (I + kChunkK - 1) / kChunkK;
     s.mg = P <= 2 * E ? 1 : P <= 6 * E ? 2 : 4;
-    // enough workgroups of FC2 for two a compute unit, while a wave still has a few chunks
+    // enough workgroups of FC2 for two a compute unit, while a wave still has two
+    // chunks (16 tokens of the figures in kernels_moe_few.h: 41.5 us with 512
+    // workgroups and with 256, 46.6 with 1024)
     int64_t S = NU <= kFewCounters ? (512 + NU - 1) / NU : 1;
     const int64_t chunks = (P < E ? P : E) * KC;
     const int64_t most = chunks / (kFewWaves * 2);
@@ -54,8 +56,8 @@ nvfp4_status sizes(const char* fn, int64_t T, int64_t k, int64_t E, int64_t H, i
 template <int MG, bool F16, bool PRE, int ACT>
 void launch_fc1(const FewArgs& f, hipStream_t st) {
     constexpr int NT = ACT == kActSiluGlu ? 2 : 1;
-    hipLaunchKernelGGL((k_moe_few_fc1<MG, 4, F16, PRE, ACT>), dim3((unsigned)((f.NU1 + NT - 1) / NT), (unsigned)f.P + 1),
-                       dim3(256), 0, st, f);
+    hipLaunchKernelGGL((k_moe_few_fc1<MG, F16, PRE, ACT>), dim3((unsigned)((f.NU1 + NT - 1) / NT), (unsigned)f.P + 1),
+                       dim3(kFewWaves1 * 64), 0, st, f);
 }
 template <int MG, bool F16, bool PRE>
 void launch_fc2(const FewArgs& f, hipStream_t st) {
