@@ -10,14 +10,14 @@
 // the matrix instructions' operand type.
 //
 // Both kernels contract as the small-M GEMM does (kernels_gemm.h) and read
-// each active expert's weights once while it has at most 4 MG rows.  What
+// each active expert's weights once for every four of its rows.  What
 // bounds them is HBM, behind a chain of latencies (ids, rows, weights).
 //
 // There is no routing launch.  k_moe_few_fc1 has a grid row per pair, and every
-// (4 MG)th pair of an expert has workgroups, which do it and those after it up
+// fourth pair of an expert has workgroups, which do it and those after it up
 // to the next.  (With an expert's pairs in one workgroup, one pass after another,
 // the busiest expert decides.)  One more workgroup makes the second kernel's list meanwhile: items of an expert
-// and up to 4 MG of its pairs.  A workgroup of k_moe_few_fc2 owns 16 columns of
+// and up to four of its pairs.  A workgroup of k_moe_few_fc2 owns 16 columns of
 // out and a share of the items' K chunks, cut evenly into one stretch per wave,
 // which a wave's ring of loads streams without a stop where an expert ends.  So
 // the sum over a token's experts needs no exchange of rows: it is formed where
@@ -32,6 +32,12 @@ namespace nvfp4 {
 
 constexpr int kFewTokens = 64;
 constexpr int kFewPairs = 512;
+// Rows of an item.  The products take four rows at a time; an expert with more
+// has its weights read again, which the caches answer: items of 8 or 16 rows
+// cost more in registers and empty rows than they save (64 tokens of 128
+// experts, top-8, 2048 x 768: 128 us with 4, 145 with 8, 174 with 16; 64 of 8,
+// top-2, 4096 x 2048, where each has 16 rows: 94, 88, 95).
+constexpr int kFewRows = 4;
 // Shapes (us of the layer in a graph: 1 token of 128 experts, top-8, 2048 x 768;
 // 16 tokens of it; 5 tokens of 8 experts, top-2, 4096 x 14336):
 //   FC1, waves and depth of their rings: 4 and 2 13.6 / 40.8 / 89.1; 4 and 4 13.7
@@ -42,7 +48,7 @@ constexpr int kFewPairs = 512;
 constexpr int kFewWaves1 = 4, kFewDepth1 = 2;
 constexpr int kFewWaves = 8, kFewDepth = 4;
 
-// Up to 4 MG pairs of one expert: places first .. first + rows - 1 of the list.
+// Up to kFewRows pairs of one expert: places first .. first + rows - 1 of the list.
 struct FewItem {
     int32_t e, first, rows;
     float g;   // the expert's global scale
@@ -76,7 +82,7 @@ struct FewArgs {
 
 // The second kernel's list, by one workgroup: a pair's place is that of its
 // expert's first pair, plus the pairs of the expert before it.
-template <int MG, int THREADS>
+template <int THREADS>
 __device__ __forceinline__ void few_list(const FewArgs& f, int32_t* ids, int32_t* place) {
     __shared__ int32_t s_sums[THREADS / 64][2];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
@@ -94,7 +100,7 @@ __device__ __forceinline__ void few_list(const FewArgs& f, int32_t* ids, int32_t
                 before += same && q < p;
             }
         const bool first = valid && before == 0;
-        const int n = first ? all : 0, its = (n + 4 * MG - 1) / (4 * MG);
+        const int n = first ? all : 0, its = (n + kFewRows - 1) / (kFewRows);
         int a = n, b = its;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -116,7 +122,7 @@ __device__ __forceinline__ void few_list(const FewArgs& f, int32_t* ids, int32_t
             place[p] = ra;
             const float g = global_scale_at(f.g2, e, f.g_div);
             for (int i = 0; i < its; ++i)
-                f.list->item[rb + i] = FewItem{e, ra + 4 * MG * i, n - 4 * MG * i < 4 * MG ? n - 4 * MG * i : 4 * MG, g};
+                f.list->item[rb + i] = FewItem{e, ra + kFewRows * i, n - kFewRows * i < kFewRows ? n - kFewRows * i : kFewRows, g};
         }
         __syncthreads();
     }
@@ -134,12 +140,12 @@ __device__ __forceinline__ void few_list(const FewArgs& f, int32_t* ids, int32_t
 }
 
 // Grid: (units of W1 / NT, pairs + 1).  NT = 2 with the gate (a pair of units: gate, up).
-template <int MG, bool F16, bool PRE, int ACT>
+template <bool F16, bool PRE, int ACT>
 __global__ void __launch_bounds__(kFewWaves1 * 64) k_moe_few_fc1(FewArgs f) {
     constexpr int W = kFewWaves1;
     constexpr int NT = ACT == kActSiluGlu ? 2 : 1;
     constexpr int RLD = NT * 16;
-    __shared__ float red[W][4 * MG * RLD];
+    __shared__ float red[W][kFewRows * RLD];
     __shared__ float2 lut[256];
     __shared__ int32_t tokens[kFewPairs];   // (few_list's first)
     __shared__ int32_t pairs[kFewPairs];
@@ -147,7 +153,7 @@ __global__ void __launch_bounds__(kFewWaves1 * 64) k_moe_few_fc1(FewArgs f) {
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int p = (int)blockIdx.y - 1, u0 = blockIdx.x * NT;
     if (p < 0) {   // first in the grid: it is not what the launch waits for in the end
-        if (blockIdx.x == 0) few_list<MG, W * 64>(f, tokens, pairs);
+        if (blockIdx.x == 0) few_list<W * 64>(f, tokens, pairs);
         return;
     }
     const int e = f.ids[p];
@@ -161,15 +167,15 @@ __global__ void __launch_bounds__(kFewWaves1 * 64) k_moe_few_fc1(FewArgs f) {
         if (q0 <= p) place += __popcll(same & (q0 + 64 <= p ? ~0ull : (1ull << (p - q0)) - 1));
         if (q0 + 64 > p && (same >> lane) & 1ull) {
             const int at = upto + __popcll(same & ((1ull << lane) - 1)) - place;
-            if (at >= 0 && at < 4 * MG) {
+            if (at >= 0 && at < kFewRows) {
                 pairs[at] = q;
                 tokens[at] = q / f.k;
             }
         }
         upto += __popcll(same);
     }
-    if (place % (4 * MG) != 0) return;
-    const int rows = upto - place < 4 * MG ? upto - place : 4 * MG;
+    if (place % (kFewRows) != 0) return;
+    const int rows = upto - place < kFewRows ? upto - place : kFewRows;
     const int c0 = f.KC1 * w / W, c1 = f.KC1 * (w + 1) / W;
     const int64_t blk0 = f.w1.block(e, u0, 0);
     const WaveWeights ww{f.w1.codes + blk0 * kCodeBlock, f.w1.scales + blk0 * kScaleBlock,
@@ -181,7 +187,7 @@ __global__ void __launch_bounds__(kFewWaves1 * 64) k_moe_few_fc1(FewArgs f) {
         asm volatile("s_barrier" ::: "memory");
     };
     const float gv = global_scale_at(f.g1, e, f.g_div);
-    small_m_pass<MG, NT, kFewDepth1, false, F16, PRE>(f.x, f.ld_x, rows, f.pre1, ww, c0, c1, f.H, lut, red[w], RLD, lane,
+    small_m_pass<1, NT, kFewDepth1, false, F16, PRE>(f.x, f.ld_x, rows, f.pre1, ww, c0, c1, f.H, lut, red[w], RLD, lane,
                                                      mid, tokens);
     __syncthreads();
     for (int t = threadIdx.x; t < rows * 16; t += W * 64) {
@@ -208,7 +214,7 @@ struct FewShared {
 
 // Grid: (units of W2, S).  A wave's stretch of the items' chunks is streamed
 // by one ring; sums[token][16] of each wave in dynamic LDS.
-template <int MG, bool F16, bool PRE>
+template <bool F16, bool PRE>
 __global__ void __launch_bounds__(kFewWaves * 64) k_moe_few_fc2(FewArgs f) {
     __shared__ FewShared sh;
     extern __shared__ float sums[];   // [kFewWaves][T * 16]
@@ -239,28 +245,19 @@ __global__ void __launch_bounds__(kFewWaves * 64) k_moe_few_fc2(FewArgs f) {
         At ld = {(int)(lo / f.KC2), (int)(lo % f.KC2)}, us = ld;
         int64_t ld_i = 0;
         const uint8_t *codes = nullptr, *scales = nullptr;   // the load side's unit
-        uint32_t row[MG];
+        uint32_t row;   // the byte offset of this lane's activation row
         auto enter = [&]() {   // the load side's item
             const int e = __builtin_amdgcn_readfirstlane(sh.item[ld.item].e);
             const int first = sh.item[ld.item].first, rows = sh.item[ld.item].rows;
             const int64_t blk = f.w2.block(e, u, 0);
             codes = f.w2.codes + blk * kCodeBlock;
             scales = f.w2.scales + blk * kScaleBlock;
-#pragma unroll
-            for (int mg = 0; mg < MG; ++mg) {
-                const int m = 4 * mg + ai;
-                row[mg] = (uint32_t)(sh.pair[first + (m < rows ? m : 0)] * f.ld_a * 2);
-            }
+            row = (uint32_t)(sh.pair[first + (ai < rows ? ai : 0)] * f.ld_a * 2);
         };
         enter();
-        f32x4 acc[1][MG];
-        auto zero = [&]() {
-#pragma unroll
-            for (int mg = 0; mg < MG; ++mg) acc[0][mg] = f32x4{0.f, 0.f, 0.f, 0.f};
-        };
-        zero();
+        f32x4 acc[1][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}};
         const uint8_t* ab = reinterpret_cast<const uint8_t*>(f.a);
-        auto load = [&](SmallSlot<MG, 1>& slot, int64_t i) {
+        auto load = [&](SmallSlot<1, 1>& slot, int64_t i) {
             if (i > ld_i) {   // i is the last one, or one more
                 ld_i = i;
                 if (++ld.chunk == f.KC2) {
@@ -274,36 +271,32 @@ __global__ void __launch_bounds__(kFewWaves * 64) k_moe_few_fc2(FewArgs f) {
             slot.sw[0] = load_scale_dword(scales + off * kScaleBlock, lane);
             const int kk = ld.chunk * kChunkK + kpiece;
             const uint32_t kb = kk < f.I ? (uint32_t)(kk * 2) : 0u;
-#pragma unroll
-            for (int mg = 0; mg < MG; ++mg) slot.xa[mg] = *reinterpret_cast<const uint4*>(ab + (row[mg] + kb));
+            slot.xa[0] = *reinterpret_cast<const uint4*>(ab + (row + kb));
             if constexpr (PRE) slot.pa = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(f.pre2) + kb);
         };
-        auto use = [&](const SmallSlot<MG, 1>& slot, int64_t i) {
-            small_m_chunk<MG, 1, false, F16, PRE>(slot, us.chunk * kChunkK + kpiece < f.I, sh.lut, lane, acc);
+        auto use = [&](const SmallSlot<1, 1>& slot, int64_t i) {
+            small_m_chunk<1, 1, false, F16, PRE>(slot, us.chunk * kChunkK + kpiece < f.I, sh.lut, lane, acc);
             const bool ends = us.chunk == f.KC2 - 1;
             if (ends || i == n - 1) {
                 // the item's rows into the tokens' sums: lane l < 16 has column l
                 const int first = sh.item[us.item].first, rows = sh.item[us.item].rows;
                 const float gv = sh.item[us.item].g;
 #pragma unroll
-                for (int mg = 0; mg < MG; ++mg)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        float v = acc[0][mg][r];
-                        v += __shfl_xor(v, 16);
-                        v += __shfl_xor(v, 32);
-                        if (lane < 16 && 4 * mg + r < rows) {
-                            const int at = first + 4 * mg + r;
-                            float* to = mine + sh.pair[at] / f.k * 16 + lane;
-                            *to = __builtin_fmaf(sh.weight[at] * gv, v, *to);
-                        }
+                for (int r = 0; r < kFewRows; ++r) {
+                    float v = acc[0][0][r];
+                    v += __shfl_xor(v, 16);
+                    v += __shfl_xor(v, 32);
+                    if (lane < 16 && r < rows) {
+                        float* to = mine + sh.pair[first + r] / f.k * 16 + lane;
+                        *to = __builtin_fmaf(sh.weight[first + r] * gv, v, *to);
                     }
-                zero();
+                }
+                acc[0][0] = f32x4{0.f, 0.f, 0.f, 0.f};
             }
             if (ends) ++us.item, us.chunk = 0;
             else ++us.chunk;
         };
-        SmallSlot<MG, 1> ring[kFewDepth];
+        SmallSlot<1, 1> ring[kFewDepth];
         const int64_t last = n - 1;
 #pragma unroll
         for (int d = 0; d < kFewDepth; ++d) {

@@ -15,14 +15,13 @@ constexpr int64_t kFewCounters = NVFP4_MOE_LAYER_COUNTER_BYTES / 4;   // units w
 constexpr int64_t kFewLd = (int64_t)1 << 22;                          // offsets of 512 rows fit 32 bits
 
 struct FewShape {
-    int mg, S;
+    int S;
     int64_t a_at, list_at, part_at, total;   // workspace: counters, a, FC2's list, partial sums
 };
 
 FewShape few_shape(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
     FewShape s;
     const int64_t P = T * k, NU = (H + kUnitN - 1) / kUnitN, KC = (I + kChunkK - 1) / kChunkK;
-    s.mg = P <= 2 * E ? 1 : P <= 6 * E ? 2 : 4;
     // enough workgroups of FC2 for two a compute unit, while a wave still has two
     // chunks (16 tokens of the figures in kernels_moe_few.h: 41.5 us with 512
     // workgroups and with 256, 46.6 with 1024)
@@ -53,28 +52,22 @@ nvfp4_status sizes(const char* fn, int64_t T, int64_t k, int64_t E, int64_t H, i
     return NVFP4_OK;
 }
 
-template <int MG, bool F16, bool PRE, int ACT>
+template <bool F16, bool PRE, int ACT>
 void launch_fc1(const FewArgs& f, hipStream_t st) {
     constexpr int NT = ACT == kActSiluGlu ? 2 : 1;
-    hipLaunchKernelGGL((k_moe_few_fc1<MG, F16, PRE, ACT>), dim3((unsigned)((f.NU1 + NT - 1) / NT), (unsigned)f.P + 1),
+    hipLaunchKernelGGL((k_moe_few_fc1<F16, PRE, ACT>), dim3((unsigned)((f.NU1 + NT - 1) / NT), (unsigned)f.P + 1),
                        dim3(kFewWaves1 * 64), 0, st, f);
 }
-template <int MG, bool F16, bool PRE>
+template <bool F16, bool PRE>
 void launch_fc2(const FewArgs& f, hipStream_t st) {
-    hipLaunchKernelGGL((k_moe_few_fc2<MG, F16, PRE>), dim3((unsigned)f.NU2, (unsigned)f.sk.S), dim3(kFewWaves * 64),
+    hipLaunchKernelGGL((k_moe_few_fc2<F16, PRE>), dim3((unsigned)f.NU2, (unsigned)f.sk.S), dim3(kFewWaves * 64),
                        (size_t)kFewWaves * f.T * 16 * sizeof(float), st, f);
 }
-template <int MG, bool F16>
-void launch(const FewArgs& f, int act, hipStream_t st) {
-    if (act == kActSiluGlu) f.pre1 ? launch_fc1<MG, F16, true, kActSiluGlu>(f, st) : launch_fc1<MG, F16, false, kActSiluGlu>(f, st);
-    else f.pre1 ? launch_fc1<MG, F16, true, kActRelu2>(f, st) : launch_fc1<MG, F16, false, kActRelu2>(f, st);
-    f.pre2 ? launch_fc2<MG, F16, true>(f, st) : launch_fc2<MG, F16, false>(f, st);
-}
 template <bool F16>
-void launch_mg(const FewArgs& f, int mg, int act, hipStream_t st) {
-    if (mg == 1) launch<1, F16>(f, act, st);
-    else if (mg == 2) launch<2, F16>(f, act, st);
-    else launch<4, F16>(f, act, st);
+void launch(const FewArgs& f, int act, hipStream_t st) {
+    if (act == kActSiluGlu) f.pre1 ? launch_fc1<F16, true, kActSiluGlu>(f, st) : launch_fc1<F16, false, kActSiluGlu>(f, st);
+    else f.pre1 ? launch_fc1<F16, true, kActRelu2>(f, st) : launch_fc1<F16, false, kActRelu2>(f, st);
+    f.pre2 ? launch_fc2<F16, true>(f, st) : launch_fc2<F16, false>(f, st);
 }
 
 }  // namespace
@@ -151,8 +144,8 @@ nvfp4_status nvfp4_moe_layer(const void* x, int64_t ld_x, const int32_t* topk_id
     f.NU2 = (int)L2.NU;
     f.KC2 = (int)L2.KC;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    if (f16) launch_mg<true>(f, sh.mg, act, st);
-    else launch_mg<false>(f, sh.mg, act, st);
+    if (f16) launch<true>(f, act, st);
+    else launch<false>(f, act, st);
     return launched(fn);
 }
 
