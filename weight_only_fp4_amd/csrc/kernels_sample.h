@@ -42,14 +42,14 @@ namespace nvfp4 {
 constexpr int kSampleThreads = 1024;
 constexpr int kSampleWaves = kSampleThreads / 64;
 constexpr int kSampleCopies = 16;      // of the 256 digits' counters: lanes of a wave mostly hit few digits
-constexpr int kSampleScanThreads = 256;
+constexpr int kSampleScanThreads = 512;
 constexpr int kSampleBins = 512;
 constexpr float kSamplePerUnit = 16.f; // bins a unit of (m - l) / t
 constexpr int kSampleListed = 2048;    // elements a slice lists
 constexpr int kSampleList = 4096;      // elements k_sample_pick sorts
 constexpr int kSampleNarrow = 256;     // above which it narrows them down first
 constexpr int kSampleMaxSlices = 64;
-constexpr int kSampleHeld = 4;         // pieces that a thread of k_sample_scan holds
+constexpr int kSampleHeld = 2;         // pieces that a thread of k_sample_scan holds
 
 // What k_sample_scan leaves of a slice.
 struct SampleSlice {
@@ -189,6 +189,19 @@ __device__ __forceinline__ void sample_values(const uint4& v, F&& f) {
     }
 }
 
+// The same of one 32-bit word of a piece, e of its first logit in the piece: the
+// loops over words stay loops, because code that runs a few times only costs
+// its fetch (eight logits unrolled in each pass: 64 x 131072 top-p 66 us, one
+// user's 131072 logits without a filter 30; so 57 and 23).
+template <int DT, typename F>
+__device__ __forceinline__ void sample_word(uint32_t w, int e, F&& f) {
+    if (DT == kLogitF32) f(e, __uint_as_float(w));
+    else {
+        f(e, act_to_f32<DT == kLogitF16>(w & 0xFFFFu));
+        f(e + 1, act_to_f32<DT == kLogitF16>(w >> 16));
+    }
+}
+
 __device__ __forceinline__ uint64_t shfl_xor_u64(uint64_t v, int m) {
     const uint32_t lo = __shfl_xor((uint32_t)v, m), hi = __shfl_xor((uint32_t)(v >> 32), m);
     return (uint64_t)hi << 32 | lo;
@@ -286,6 +299,7 @@ struct SampleShared {
     int count;
     uint32_t low, high;
 };
+static_assert(kSampleScanThreads >= kSampleBins, "a bin a thread");
 static_assert(256 * kSampleCopies == kSampleList, "the digits' room holds a list");
 
 // The element of the cut's elements that the row's order reaches at `target`:
@@ -468,7 +482,8 @@ __device__ __forceinline__ int sample_listed_bins(const SampleSettings& set) {
     return set.p < 1.f ? kSampleBins - 1 : sample_min_p_bins(set);
 }
 
-// Grid: (slices, rows).  A thread's pieces are 256 apart; a slice of up to
+// Grid: (slices, rows).  A thread's pieces are kSampleScanThreads
+// apart; a slice of up to
 // 1024 is read once and stays in LDS.
 template <int DT>
 __global__ void __launch_bounds__(kSampleScanThreads) k_sample_scan(SampleArgs a) {
@@ -481,12 +496,17 @@ __global__ void __launch_bounds__(kSampleScanThreads) k_sample_scan(SampleArgs a
     const SampleRow<DT> row(a, b);
     const int c0 = s * a.slice, c1 = c0 + a.slice < row.pieces ? c0 + a.slice : row.pieces;
     constexpr int kAtOnce = kSampleHeld * kSampleScanThreads;
-    __shared__ uint4 s_held[kAtOnce];   // a thread reads what it wrote itself
+    __shared__ uint32_t s_held[kSampleHeld * 4][kSampleScanThreads];   // word by word; a thread reads what it wrote itself
     auto load = [&](int c) {
         uint4 v[kSampleHeld];
         sample_load<DT, kSampleHeld>(row, c + tid, kSampleScanThreads, c1, v);
 #pragma unroll
-        for (int h = 0; h < kSampleHeld; ++h) s_held[h * kSampleScanThreads + tid] = v[h];
+        for (int h = 0; h < kSampleHeld; ++h) {
+            s_held[4 * h][tid] = v[h].x;
+            s_held[4 * h + 1][tid] = v[h].y;
+            s_held[4 * h + 2][tid] = v[h].z;
+            s_held[4 * h + 3][tid] = v[h].w;
+        }
     };
     load(c0);
     const SampleSettings set(a, b);
@@ -496,10 +516,8 @@ __global__ void __launch_bounds__(kSampleScanThreads) k_sample_scan(SampleArgs a
         for (int c = c0; c < c1; c += kAtOnce) {
             if (a.slice > kAtOnce) load(c);
 #pragma unroll 1
-            for (int h = 0; h < kSampleHeld; ++h) {
-                const int i0 = (c + tid + h * kSampleScanThreads) * P - row.skew;
-                sample_values<DT>(s_held[h * kSampleScanThreads + tid], [&](int e, float l) { f(i0 + e, l); });
-            }
+            for (int j = 0; j < 4 * kSampleHeld; ++j)
+                sample_word<DT>(s_held[j][tid], (c + tid + (j >> 2) * kSampleScanThreads) * P - row.skew + (j & 3) * (P / 4), f);
         }
     };
     for (int i = tid; i < kSampleBins; i += kSampleScanThreads) s_bins[i] = 0;
@@ -552,8 +570,9 @@ __global__ void __launch_bounds__(kSampleScanThreads) k_sample_scan(SampleArgs a
     // down to the bin of the slice's own k-th
     int limit = sample_listed_bins(set);
     if (set.k > 0) {
-        const uint32_t n0 = (uint32_t)s_bins[2 * tid], n1 = (uint32_t)s_bins[2 * tid + 1], want = (uint32_t)set.k;
-        uint32_t upto = n0 + n1;
+        // a bin a thread, of the first kSampleBins
+        const uint32_t n = tid < kSampleBins ? (uint32_t)s_bins[tid] : 0u, want = (uint32_t)set.k;
+        uint32_t upto = n;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
             const uint32_t o = __shfl_up(upto, d);
@@ -562,7 +581,7 @@ __global__ void __launch_bounds__(kSampleScanThreads) k_sample_scan(SampleArgs a
         if (lane == 63) s_wave[tid >> 6] = upto;
         __syncthreads();
         for (int w = 0; w < (tid >> 6); ++w) upto += s_wave[w];
-        if (upto >= want && upto - n0 - n1 < want) s_limit = upto - n1 >= want ? 2 * tid : 2 * tid + 1;
+        if (tid < kSampleBins && upto >= want && upto - n < want) s_limit = tid;
         __syncthreads();
         limit = limit < s_limit ? limit : s_limit;
     }
@@ -638,18 +657,18 @@ __device__ __forceinline__ int sample_fill(uint64_t* list, int n) {
     return size;
 }
 
-// Bin d of the row from the slices': f(slice, content), sixteen loads in flight.
+// Bin d of the row from the slices': f(slice, content), twenty loads in flight.
 template <typename F>
 __device__ __forceinline__ void sample_join(const SampleSlice* slices, int S, const SampleShared& sh, int d, F&& f) {
-    for (int s0 = 0; s0 < S; s0 += 16) {
-        uint64_t v[16];
+    for (int s0 = 0; s0 < S; s0 += 20) {
+        uint64_t v[20];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 20; ++i) {
             const int s = s0 + i < S ? s0 + i : S - 1, at = d - sh.below[s];
             v[i] = slices[s].bins[at > 0 ? at : 0];
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int i = 0; i < 20; ++i)
             if (s0 + i < S && d >= sh.below[s0 + i]) f(s0 + i, v[i]);
     }
 }
@@ -986,25 +1005,33 @@ __device__ __forceinline__ bool sample_summed(const SampleArgs& a, int b, const 
     for (int c = c0; c < c1; c += kSampleThreads) {
         uint4 loaded[1];
         sample_load<DT, 1>(row, c + tid, 0, c1, loaded);
-        const uint4 v = loaded[0];
+        uint32_t* words = reinterpret_cast<uint32_t*>(sh.second);   // word by word; a thread reads what it wrote itself
+        words[tid] = loaded[0].x;
+        words[kSampleThreads + tid] = loaded[0].y;
+        words[2 * kSampleThreads + tid] = loaded[0].z;
+        words[3 * kSampleThreads + tid] = loaded[0].w;
         const int i0 = (c + tid) * P - row.skew;
-        uint64_t q[P], mine = 0, step;
-        sample_values<DT>(v, [&](int e, float l) {
-            q[e] = keeps(i0 + e, l) ? units_in(s, l) : 0;
-            mine += q[e];
-        });
+        uint64_t mine = 0, step;
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j)
+            sample_word<DT>(words[j * kSampleThreads + tid], i0 + j * (P / 4), [&](int i, float l) {
+                if (keeps(i, l)) mine += units_in(s, l);
+            });
         const uint64_t end = upto_here + sample_scan<uint64_t>(mine, sh.sums, step);
         if (end > want && end - mine <= want) {
             uint64_t at = end - mine;
             bool done = false;
-            sample_values<DT>(v, [&](int e, float l) {
-                at += q[e];
-                if (!done && at > want) {
-                    done = true;
-                    a.tokens[b] = i0 + e;
-                    if (a.logprobs) a.logprobs[b] = sw.logprob(l, kept_total);
-                }
-            });
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j)
+                sample_word<DT>(words[j * kSampleThreads + tid], i0 + j * (P / 4), [&](int i, float l) {
+                    if (done || !keeps(i, l)) return;
+                    at += units_in(s, l);
+                    if (at > want) {
+                        done = true;
+                        a.tokens[b] = i;
+                        if (a.logprobs) a.logprobs[b] = sw.logprob(l, kept_total);
+                    }
+                });
         }
         upto_here += step;
         if (upto_here > want) break;   // the same in every thread
