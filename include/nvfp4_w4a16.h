@@ -709,7 +709,7 @@ nvfp4_status nvfp4_lora_add(const void* x, int64_t ld_x, const void* a, int64_t 
  *   blob of nvfp4_repack_gated (NVFP4_MOE_SILU_GLU) or nvfp4_repack
  *   (NVFP4_MOE_RELU2) of E experts, I and H; w_fc2 of nvfp4_repack (E, H, I);
  *   global scales fp32 [E], or NULL with mx (blobs of mxfp4_repack_gated /
- *   mxfp4_repack); out [T][ld_o] of H values, not x.
+ *   mxfp4_repack); out [T][ld_o] of H values (may be x).
  *   workspace: nvfp4_moe_layer_workspace_bytes(T, k, E, H, I) bytes, 256-byte
  *   aligned, its first NVFP4_MOE_LAYER_COUNTER_BYTES zero before its first use;
  *   every call leaves them zero, so one workspace serves any number of these

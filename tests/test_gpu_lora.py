@@ -75,6 +75,19 @@ def test_in_place_strided_and_misaligned(T):
     assert (by[:, :3] == 7).all() and (by[:, 3 + N:] == 7).all()
 
 
+def test_two_calls_at_once_on_two_streams():
+    calls = [make(60, 1024, 500, 32, 7, BF, seed=s) for s in (1, 2)]
+    want = [nv.lora_add(*c[:5], scale=c[5]) for c in calls]
+    torch.cuda.synchronize()
+    got, streams = [], [torch.cuda.Stream() for _ in calls]
+    for _ in range(5):
+        for c, st in zip(calls, streams):
+            with torch.cuda.stream(st):
+                got.append(nv.lora_add(*c[:5], scale=c[5]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want[i % 2]) for i, g in enumerate(got))
+
+
 def test_large_and_small_values_in_fp16():
     """x A^T beyond fp16's range, and far below it."""
     for sigma in (60000.0, 2.0 ** -22):

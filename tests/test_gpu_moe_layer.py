@@ -115,6 +115,19 @@ def test_strided_rows_given_output_and_the_rows_next_to_it():
     assert (bo[0] == 5).all() and (bo[10] == 5).all() and (bo[:, :3] == 5).all() and (bo[:, 259:] == 5).all()
 
 
+def test_output_over_the_input_and_on_another_stream():
+    layer = Layer(8, 256, 128, BF, seed=6)
+    x, ids, w = layer.tokens(9, 2)
+    want = layer.run(x, ids, w)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        y = x.clone()
+        got = layer.run(y, ids, w, out=y)
+    side.synchronize()
+    assert got.data_ptr() == y.data_ptr() and torch.equal(got, want)
+
+
 def test_a_token_does_not_depend_on_the_others_values():
     layer = Layer(8, 256, 128, BF, seed=7)
     x, ids, w = layer.tokens(12, 3)

@@ -120,6 +120,39 @@ def test_infinities_nan_zeros_and_empty_rows(dtype):
         check(y, [u] * 8, t=[inf] * 8, min_p=[0.2] * 8)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_slices_of_several_reads_and_very_long_rows(dtype):
+    """So many rows that a slice is more than a workgroup holds, and rows of the most slices."""
+    rng = np.random.default_rng(7)
+    B = 300
+    x = logits_of(B, 40001, dtype, 8)
+    k = [int(v) for v in rng.choice([0, 1, 40, 700], B)]
+    check(x, rng.random(B), t=rng.choice([0.0, 0.7, 1.3], B), k=k, p=rng.choice([0.5, 0.9, 1.0], B),
+          min_p=rng.choice([0.0, 0.05], B))
+    x = logits_of(1, 1200007, dtype, 9)
+    for kw in (dict(), dict(k=[300]), dict(p=[0.8]), dict(min_p=[0.03]), dict(t=[0.0])):
+        check(x, rng.random(1), **kw)
+
+
+def test_long_lists():
+    """More candidates than a slice or a row lists: the row itself is read again."""
+    rng = np.random.default_rng(8)
+    x = logits_of(4, 60000, "fp32", 10)
+    check(x, rng.random(4), k=[5000, 9000, 2500, 59999], p=[1.0, 0.9, 0.7, 0.99])
+    check(x * 0.02, rng.random(4), p=[0.1, 0.5, 0.9, 0.999])
+    check(x * 0.02, rng.random(4), min_p=[0.9, 0.99, 0.95, 0.5], p=[1.0, 0.9, 1.0, 0.9])
+
+
+@pytest.mark.parametrize("large", [3e5, 1e6, 1e8, 1e30])
+def test_logits_far_from_zero(large):
+    """Grids whose bins are finer than the logits' own steps."""
+    rng = np.random.default_rng(9)
+    x = logits_of(5, 9000, "fp32", 11)
+    for y in (x + large, x - large, x * large):
+        for kw in (dict(), dict(k=[30] * 5), dict(p=[0.7] * 5), dict(min_p=[0.2] * 5), dict(min_p=[0.2] * 5, p=[0.9] * 5)):
+            check(y, rng.random(5), t=rng.uniform(0.3, 3, 5), **kw)
+
+
 def test_random_numbers_at_their_ends():
     x = logits_of(7, 999, "fp32", 3)
     check(x, [0.0, 1.0 - 2.0 ** -24, 1.0, 7.0, -1.0, float("nan"), 2.0 ** -24])

@@ -161,7 +161,6 @@ PyObject* moe_layer(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const float *g1 = per_expert(a[7], "g1"), *g2 = per_expert(a[8], "g2");
     const void *p1 = per_column(a[11], "pre_scale1", H), *p2 = per_column(a[12], "pre_scale2", I);
     at::Tensor out = output(a[14], "out", type, {T, H}, dev);
-    TORCH_CHECK_VALUE(T == 0 || out.data_ptr() != x.data_ptr(), "out must not be x");
     at::Tensor ws = workspace_of(a[15], need, NVFP4_MOE_LAYER_COUNTER_BYTES, dev);
     check(nvfp4_moe_layer(x.data_ptr(), leading(x), ints(ids), static_cast<const float*>(weights.data_ptr()), T, k, p1, w1, g1,
                           p2, w2, g2, truth(a[9]), (int)activation, out.data_ptr(), leading(out), E, H, I, ws.data_ptr(),
