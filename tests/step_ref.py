@@ -71,8 +71,9 @@ def weights(codes, scales, mx):
 
 
 def moe(x, ids, topk_weights, w1, w2, g1, g2, inter, gated=True, mx=False, pre1=None, pre2=None):
-    """(out, bound) as float64 numpy; w1, w2 (codes, scales) per expert.  Roundings: X' and a' (if scaled), a and the
-    output, half a step each; sums in fp32, n 2^-24 of the terms' absolute sum each."""
+    """(out, bound) as float64 numpy; w1, w2 (codes, scales) per expert.  Roundings: X' (if scaled) and the output, half a
+    step each; a to two parts of its type (half a step of half a step; in fp16 not below half its least step); sums in
+    fp32, n 2^-24 of the terms' absolute sum each (twice n in the second, for the two parts)."""
     dt = x.dtype
     u = 2.0 ** -8 if dt == torch.bfloat16 else 2.0 ** -11
     tiny = 0.0 if dt == torch.bfloat16 else 2.0 ** -25
@@ -102,12 +103,10 @@ def moe(x, ids, topk_weights, w1, w2, g1, g2, inter, gated=True, mx=False, pre1=
             else:
                 a = np.maximum(h, 0) ** 2
                 da = (2 * np.maximum(h, 0) + dh) * dh + a * 2.0 ** -22
-            da = da + u * (np.abs(a) + da) + tiny
-            ap, dap = a * p2, da * np.abs(p2)
-            if pre2 is not None:
-                dap = dap + u * (np.abs(ap) + dap) + tiny
+            ap, dap = a * p2, da * np.abs(p2) + np.abs(a * p2) * 2.0 ** -24
+            dap = dap + u * u * (np.abs(ap) + dap) + tiny
             y = m2 @ ap
-            dy = np.abs(m2) @ (dap + (inter + 64) * 2.0 ** -24 * np.abs(ap))
+            dy = np.abs(m2) @ (dap + (2 * inter + 64) * 2.0 ** -24 * np.abs(ap))
             out[t] += w * s2 * y
             slack[t] += abs(w * s2) * (dy + np.abs(y) * 2.0 ** -21)
     return out, slack + u * (np.abs(out) + slack) + tiny

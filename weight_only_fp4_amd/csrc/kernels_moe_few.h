@@ -1,13 +1,14 @@
 // A whole mixture-of-experts layer for a few tokens in two kernels
 // (nvfp4_moe_layer).  With pairs p = t k + j, e = ids[p]:
 //
-//   a_p   = RNE16(act(g1_e X'_t W1_e^T))                 k_moe_few_fc1
-//   out_t = RNE16(sum_j w_tj g2_e (a'_p W2_e^T))         k_moe_few_fc2
+//   a_p   = act(g1_e X'_t W1_e^T) (* the second pre-quant scale)   k_moe_few_fc1
+//   out_t = RNE16(sum_j w_tj g2_e (a_p W2_e^T))                    k_moe_few_fc2
 //
-// X' and a' with the pre-quant scales applied (RNE16) where given.  The first
-// product's sums stay fp32 through the activation, and the second's through
-// the weighted sum: a is the only value between x and out that is rounded, to
-// the matrix instructions' operand type.
+// X' with the first pre-quant scale applied (RNE16) where given.  Sums stay fp32
+// from x to out; a is handed on as two 16-bit parts, the rounded value and what
+// the rounding took off, each a row of the second product (16 bits in bf16, 22
+// in fp16: with the rounded value alone the layer's error was 1.4 to 1.55 times
+// that of rounding the output; 16 tokens took 45 us for 47).
 //
 // Both kernels contract as the small-M GEMM does (kernels_gemm.h) and read
 // each active expert's weights once for every four of its rows.  What
@@ -16,12 +17,18 @@
 // There is no routing launch.  k_moe_few_fc1 has a grid row per pair, and every
 // fourth pair of an expert has workgroups, which do it and those after it up
 // to the next.  (With an expert's pairs in one workgroup, one pass after another,
-// the busiest expert decides.)  One more workgroup makes the second kernel's list meanwhile: items of an expert
-// and up to four of its pairs.  A workgroup of k_moe_few_fc2 owns 16 columns of
-// out and a share of the items' K chunks, cut evenly into one stretch per wave,
-// which a wave's ring of loads streams without a stop where an expert ends.  So
-// the sum over a token's experts needs no exchange of rows: it is formed where
-// the products are, and split workgroups exchange 16 columns of T rows.
+// the busiest expert decides.)  One more workgroup makes the second kernel's
+// list meanwhile: items of an expert and up to four of its pairs.  A workgroup
+// of k_moe_few_fc2 owns 16 columns of out and a share of the items' K chunks,
+// cut evenly into one stretch per wave, which a wave's ring of loads streams
+// without a stop where an expert ends.  So the sum over a token's experts needs
+// no exchange of rows: it is formed where the products are, and split workgroups
+// exchange 16 columns of T rows.
+//
+// Measured in a graph: 1 token of 128 experts, top-8, 2048 x 768 (21.2 MB of
+// weights): 13.5 us (1.6 TB/s; the chain of latencies is most of it); 16 tokens
+// of it: 47 with NVFP4 weights; 5 tokens of 8 experts, top-2, 4096 x 14336
+// (0.7 GB if each has a pair): 99 (5 to 6 of the 7 TB/s that a plain read reaches).
 //
 // Waves add into accumulators of their own and are summed in a fixed order, as
 // the splits are: no result depends on timing.
@@ -32,23 +39,29 @@ namespace nvfp4 {
 
 constexpr int kFewTokens = 64;
 constexpr int kFewPairs = 512;
-// Rows of an item.  The products take four rows at a time; an expert with more
-// has its weights read again, which the caches answer: items of 8 or 16 rows
+// Pairs of a workgroup of the first product: its rows, four at a time.  An expert
+// with more has its weights read again, which the caches answer: 8 or 16 rows
 // cost more in registers and empty rows than they save (64 tokens of 128
 // experts, top-8, 2048 x 768: 128 us with 4, 145 with 8, 174 with 16; 64 of 8,
 // top-2, 4096 x 2048, where each has 16 rows: 94, 88, 95).
 constexpr int kFewRows = 4;
+// Pairs of an item of the second product.  Their two parts are rows of it: one
+// or two pairs take one product of four rows, three or four a second one on the
+// same decoded weights (items of two pairs only: 12.9 / 48.6 / 100.4 and, 64
+// tokens of 128 experts, 146; so 13.5 / 47.2 / 99.4 and 140; the parts as two
+// products of four pairs' rows: 13.1 / 47.6 / 100.2 and 140).
+constexpr int kFewItem = 4;
 // Shapes (us of the layer in a graph: 1 token of 128 experts, top-8, 2048 x 768;
 // 16 tokens of it; 5 tokens of 8 experts, top-2, 4096 x 14336):
 //   FC1, waves and depth of their rings: 4 and 2 13.6 / 40.8 / 89.1; 4 and 4 13.7
 //   / 44.2 / 90.5; 2 and 4 14.8 / 41.5 / 87.4; 1 and 4 15.5 / 43.2 / 87.0; 8 and 2
-//   13.8 / 49.0 / 93.2;
-//   FC2 (with 2 and 4 for FC1): 8 and 4 14.8 / 41.5 / 87.4; 8 and 2 14.2 / 42.1 /
-//   87.6; 4 and 4 14.7 / 42.7 / 88.1; 16 and 2 13.0 / 44.8 / 90.2.
+//   13.8 / 49.0 / 93.2 (with a in one part);
+//   FC2: 8 and 2 13.5 / 47.2 / 99.4; 8 and 3 17.3 / 51.3 / 102.7 (more than 128
+//   registers: one workgroup a compute unit); 4 and 2 14.0 / 49.3 / 100.0.
 constexpr int kFewWaves1 = 4, kFewDepth1 = 2;
-constexpr int kFewWaves = 8, kFewDepth = 4;
+constexpr int kFewWaves = 8, kFewDepth = 2;
 
-// Up to kFewRows pairs of one expert: places first .. first + rows - 1 of the list.
+// Up to kFewItem pairs of one expert: places first .. first + rows - 1 of the list.
 struct FewItem {
     int32_t e, first, rows;
     float g;   // the expert's global scale
@@ -70,10 +83,10 @@ struct FewArgs {
     const float* g2;
     const uint16_t* pre1;
     const uint16_t* pre2;
-    uint16_t* a;          // [P][ld_a] workspace
+    uint16_t* a;          // [P][2][I] workspace: the rounded values, the rests
     FewList* list;        // workspace
     uint16_t* out;
-    int64_t ld_a, ld_o;
+    int64_t ld_o;
     SplitK sk;            // k_moe_few_fc2's splits: partials [S][units][T * 16], counters [units]
     int g_div;
     int T, k, P, E, H, I, F;   // F: rows of W1 (2 I with a gate)
@@ -100,7 +113,7 @@ __device__ __forceinline__ void few_list(const FewArgs& f, int32_t* ids, int32_t
                 before += same && q < p;
             }
         const bool first = valid && before == 0;
-        const int n = first ? all : 0, its = (n + kFewRows - 1) / (kFewRows);
+        const int n = first ? all : 0, its = (n + kFewItem - 1) / kFewItem;
         int a = n, b = its;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -122,7 +135,7 @@ __device__ __forceinline__ void few_list(const FewArgs& f, int32_t* ids, int32_t
             place[p] = ra;
             const float g = global_scale_at(f.g2, e, f.g_div);
             for (int i = 0; i < its; ++i)
-                f.list->item[rb + i] = FewItem{e, ra + kFewRows * i, n - kFewRows * i < kFewRows ? n - kFewRows * i : kFewRows, g};
+                f.list->item[rb + i] = FewItem{e, ra + kFewItem * i, n - kFewItem * i < kFewItem ? n - kFewItem * i : kFewItem, g};
         }
         __syncthreads();
     }
@@ -174,7 +187,7 @@ __global__ void __launch_bounds__(kFewWaves1 * 64) k_moe_few_fc1(FewArgs f) {
         }
         upto += __popcll(same);
     }
-    if (place % (kFewRows) != 0) return;
+    if (place % kFewRows != 0) return;
     const int rows = upto - place < kFewRows ? upto - place : kFewRows;
     const int c0 = f.KC1 * w / W, c1 = f.KC1 * (w + 1) / W;
     const int64_t blk0 = f.w1.block(e, u0, 0);
@@ -199,8 +212,15 @@ __global__ void __launch_bounds__(kFewWaves1 * 64) k_moe_few_fc1(FewArgs f) {
             if (NT == 2) s1 += red[wi][r * RLD + (NT - 1) * 16 + c];
         }
         const int n = (int)blockIdx.x * 16 + c;
-        const float v = ACT == kActSiluGlu ? silu_times(gv * s0, gv * s1) : relu_squared(gv * s0);
-        if (n < f.I) f.a[(int64_t)pairs[r] * f.ld_a + n] = (uint16_t)round_out<F16>(v);
+        float v = ACT == kActSiluGlu ? silu_times(gv * s0, gv * s1) : relu_squared(gv * s0);
+        if (n < f.I) {
+            if (f.pre2) v = fp32_value(v * act_to_f32<F16>(f.pre2[n]));
+            const uint32_t hi = round_out<F16>(v);
+            const float rest = v - act_to_f32<F16>(hi);   // an infinity (or NaN) leaves nothing over
+            uint16_t* to = f.a + (int64_t)pairs[r] * 2 * f.I + n;
+            to[0] = (uint16_t)hi;
+            to[f.I] = (uint16_t)round_out<F16>(fabsf(rest) < __builtin_inff() ? rest : 0.f);
+        }
     }
 }
 
@@ -214,7 +234,7 @@ struct FewShared {
 
 // Grid: (units of W2, S).  A wave's stretch of the items' chunks is streamed
 // by one ring; sums[token][16] of each wave in dynamic LDS.
-template <bool F16, bool PRE>
+template <bool F16>
 __global__ void __launch_bounds__(kFewWaves * 64) k_moe_few_fc2(FewArgs f) {
     __shared__ FewShared sh;
     extern __shared__ float sums[];   // [kFewWaves][T * 16]
@@ -245,19 +265,24 @@ __global__ void __launch_bounds__(kFewWaves * 64) k_moe_few_fc2(FewArgs f) {
         At ld = {(int)(lo / f.KC2), (int)(lo % f.KC2)}, us = ld;
         int64_t ld_i = 0;
         const uint8_t *codes = nullptr, *scales = nullptr;   // the load side's unit
-        uint32_t row;   // the byte offset of this lane's activation row
+        uint32_t row[2];   // the byte offsets of this lane's activation rows: pairs 0 and 1, 2 and 3
         auto enter = [&]() {   // the load side's item
             const int e = __builtin_amdgcn_readfirstlane(sh.item[ld.item].e);
             const int first = sh.item[ld.item].first, rows = sh.item[ld.item].rows;
             const int64_t blk = f.w2.block(e, u, 0);
             codes = f.w2.codes + blk * kCodeBlock;
             scales = f.w2.scales + blk * kScaleBlock;
-            row = (uint32_t)(sh.pair[first + (ai < rows ? ai : 0)] * f.ld_a * 2);
+            // row ai of a group of four: part ai & 1 of its pair ai >> 1
+#pragma unroll
+            for (int mg = 0; mg < 2; ++mg) {
+                const int at = 2 * mg + (ai >> 1);
+                row[mg] = (uint32_t)((2 * sh.pair[first + (at < rows ? at : 0)] + (ai & 1)) * (int64_t)f.I * 2);
+            }
         };
         enter();
-        f32x4 acc[1][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}};
+        f32x4 acc[1][2] = {{f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}}};
         const uint8_t* ab = reinterpret_cast<const uint8_t*>(f.a);
-        auto load = [&](SmallSlot<1, 1>& slot, int64_t i) {
+        auto load = [&](SmallSlot<2, 1>& slot, int64_t i) {
             if (i > ld_i) {   // i is the last one, or one more
                 ld_i = i;
                 if (++ld.chunk == f.KC2) {
@@ -271,19 +296,30 @@ __global__ void __launch_bounds__(kFewWaves * 64) k_moe_few_fc2(FewArgs f) {
             slot.sw[0] = load_scale_dword(scales + off * kScaleBlock, lane);
             const int kk = ld.chunk * kChunkK + kpiece;
             const uint32_t kb = kk < f.I ? (uint32_t)(kk * 2) : 0u;
-            slot.xa[0] = *reinterpret_cast<const uint4*>(ab + (row + kb));
-            if constexpr (PRE) slot.pa = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(f.pre2) + kb);
+#pragma unroll
+            for (int mg = 0; mg < 2; ++mg) slot.xa[mg] = *reinterpret_cast<const uint4*>(ab + (row[mg] + kb));
         };
-        auto use = [&](const SmallSlot<1, 1>& slot, int64_t i) {
-            small_m_chunk<1, 1, false, F16, PRE>(slot, us.chunk * kChunkK + kpiece < f.I, sh.lut, lane, acc);
+        auto use = [&](const SmallSlot<2, 1>& slot, int64_t i) {
+            const bool kin = us.chunk * kChunkK + kpiece < f.I;
+            if (sh.item[us.item].rows > 2) {
+                small_m_chunk<2, 1, false, F16, false>(slot, kin, sh.lut, lane, acc);
+            } else {
+                SmallSlot<1, 1> half;
+                half.cw[0] = slot.cw[0];
+                half.sw[0] = slot.sw[0];
+                half.xa[0] = slot.xa[0];
+                f32x4 one[1][1] = {{acc[0][0]}};
+                small_m_chunk<1, 1, false, F16, false>(half, kin, sh.lut, lane, one);
+                acc[0][0] = one[0][0];
+            }
             const bool ends = us.chunk == f.KC2 - 1;
             if (ends || i == n - 1) {
                 // the item's rows into the tokens' sums: lane l < 16 has column l
                 const int first = sh.item[us.item].first, rows = sh.item[us.item].rows;
                 const float gv = sh.item[us.item].g;
 #pragma unroll
-                for (int r = 0; r < kFewRows; ++r) {
-                    float v = acc[0][0][r];
+                for (int r = 0; r < kFewItem; ++r) {
+                    float v = acc[0][r >> 1][2 * r & 3] + acc[0][r >> 1][(2 * r & 3) + 1];
                     v += __shfl_xor(v, 16);
                     v += __shfl_xor(v, 32);
                     if (lane < 16 && r < rows) {
@@ -291,12 +327,12 @@ __global__ void __launch_bounds__(kFewWaves * 64) k_moe_few_fc2(FewArgs f) {
                         *to = __builtin_fmaf(sh.weight[first + r] * gv, v, *to);
                     }
                 }
-                acc[0][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+                acc[0][0] = acc[0][1] = f32x4{0.f, 0.f, 0.f, 0.f};
             }
             if (ends) ++us.item, us.chunk = 0;
             else ++us.chunk;
         };
-        SmallSlot<1, 1> ring[kFewDepth];
+        SmallSlot<2, 1> ring[kFewDepth];
         const int64_t last = n - 1;
 #pragma unroll
         for (int d = 0; d < kFewDepth; ++d) {

@@ -12,7 +12,7 @@ namespace {
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 constexpr int64_t kFewCounters = NVFP4_MOE_LAYER_COUNTER_BYTES / 4;   // units whose columns may be split
-constexpr int64_t kFewLd = (int64_t)1 << 22;                          // offsets of 512 rows fit 32 bits
+constexpr int64_t kFewLd = (int64_t)1 << 21;                          // offsets of 512 rows in two parts fit 32 bits
 
 struct FewShape {
     int S;
@@ -32,7 +32,7 @@ FewShape few_shape(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
     if (S > 16) S = 16;
     s.S = S < 1 ? 1 : (int)S;
     s.a_at = NVFP4_MOE_LAYER_COUNTER_BYTES;
-    s.list_at = s.a_at + round_up(P * I * 2, 256);
+    s.list_at = s.a_at + round_up(P * I * 4, 256);
     s.part_at = s.list_at + round_up((int64_t)sizeof(FewList), 256);
     s.total = s.part_at + (s.S > 1 ? (int64_t)s.S * NU * T * kUnitN * 4 : 0);
     return s;
@@ -47,7 +47,7 @@ nvfp4_status sizes(const char* fn, int64_t T, int64_t k, int64_t E, int64_t H, i
     if (E < 1 || E > kMaxExperts) return fail(NVFP4_ERR_INVALID_ARG, "%s: E = %lld must be in [1, %d]", fn, (long long)E, kMaxExperts);
     const int64_t unit = mx ? 32 : 16;
     if (H < unit || I < unit || H % unit != 0 || I % unit != 0 || H >= kFewLd || I >= kFewLd)
-        return fail(NVFP4_ERR_INVALID_ARG, "%s: H = %lld, I = %lld must be multiples of %lld below 2^22", fn, (long long)H,
+        return fail(NVFP4_ERR_INVALID_ARG, "%s: H = %lld, I = %lld must be multiples of %lld below 2^21", fn, (long long)H,
                     (long long)I, (long long)unit);
     return NVFP4_OK;
 }
@@ -58,16 +58,16 @@ void launch_fc1(const FewArgs& f, hipStream_t st) {
     hipLaunchKernelGGL((k_moe_few_fc1<F16, PRE, ACT>), dim3((unsigned)((f.NU1 + NT - 1) / NT), (unsigned)f.P + 1),
                        dim3(kFewWaves1 * 64), 0, st, f);
 }
-template <bool F16, bool PRE>
+template <bool F16>
 void launch_fc2(const FewArgs& f, hipStream_t st) {
-    hipLaunchKernelGGL((k_moe_few_fc2<F16, PRE>), dim3((unsigned)f.NU2, (unsigned)f.sk.S), dim3(kFewWaves * 64),
+    hipLaunchKernelGGL((k_moe_few_fc2<F16>), dim3((unsigned)f.NU2, (unsigned)f.sk.S), dim3(kFewWaves * 64),
                        (size_t)kFewWaves * f.T * 16 * sizeof(float), st, f);
 }
 template <bool F16>
 void launch(const FewArgs& f, int act, hipStream_t st) {
     if (act == kActSiluGlu) f.pre1 ? launch_fc1<F16, true, kActSiluGlu>(f, st) : launch_fc1<F16, false, kActSiluGlu>(f, st);
     else f.pre1 ? launch_fc1<F16, true, kActRelu2>(f, st) : launch_fc1<F16, false, kActRelu2>(f, st);
-    f.pre2 ? launch_fc2<F16, true>(f, st) : launch_fc2<F16, false>(f, st);
+    launch_fc2<F16>(f, st);
 }
 
 }  // namespace
@@ -130,7 +130,6 @@ nvfp4_status nvfp4_moe_layer(const void* x, int64_t ld_x, const int32_t* topk_id
     f.P = (int)(T * k);
     f.list = reinterpret_cast<FewList*>(ws + sh.list_at);
     f.out = static_cast<uint16_t*>(out);
-    f.ld_a = I;
     f.ld_o = ld_o;
     f.sk = SplitK{sh.S, reinterpret_cast<float*>(ws + sh.part_at), reinterpret_cast<int*>(ws)};
     f.g_div = global_scale_is_divisor != 0;
