@@ -680,7 +680,8 @@ nvfp4_status nvfp4_kv_plan(const int32_t* cached, const int32_t* fresh, int64_t 
 /* Low-rank adapters beside a shared projection: with a = adapter[t],
  *   out[t] = RNE16(y[t] + scale[a] * (x[t] A_a^T) B_a^T),
  * or y[t] unchanged where a is outside [0, L).  Sums are fp32; x A_a^T enters
- * the second product with 16 (bf16) or 22 (fp16) bits.
+ * the second product with 16 (bf16) or 22 (fp16) bits, in two parts, so that an
+ * infinite value of B gives an infinity or NaN.
  *   x [T][ld_x] of K values, y and out [T][ld_y], [T][ld_o] of N (out may be y
  *   with the same leading dimension; no other overlap), a [L] matrices [R][K]
  *   (strides a_l, a_r), b [L] matrices [N][R] (strides b_l, b_n), adapter int32

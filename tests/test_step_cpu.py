@@ -69,6 +69,7 @@ def test_plan_refusals(L, kw, status, needle):
     (dict(a_r=130), ALIGN, "16-byte"), (dict(b_n=20), ALIGN, "16-byte"), (dict(y=A + 1), ALIGN, "misaligned"),
     (dict(ids=A + 2), ALIGN, "misaligned"), (dict(s=A + 2), ALIGN, "misaligned"), (dict(ws=None), SMALL, "workspace"),
     (dict(wsb=100), SMALL, "workspace"), (dict(ws=A + 8), ALIGN, "workspace"), (dict(T=0), OK, ""), (dict(N=0, ld_y=0), OK, ""),
+    (dict(ld_y=48), INVALID, "another leading"), (dict(T=0, ld_y=48), OK, ""),
 ])
 def test_lora_refusals(L, kw, status, needle):
     a = dict(x=A, ld_x=128, a=A, a_l=2048, a_r=128, b=A, b_l=512, b_n=16, ids=A, s=A, y=A, ld_y=32, o=A, ld_o=32, T=4, K=128, N=32,
@@ -80,7 +81,7 @@ def test_lora_refusals(L, kw, status, needle):
 
 
 @pytest.mark.parametrize("kw,status,needle", [
-    (dict(T=-1), INVALID, "T ="), (dict(T=65), INVALID, "up to 64"), (dict(T=64, k=9), INVALID, "512"), (dict(k=0), INVALID, "k ="),
+    (dict(T=-1), INVALID, "T ="), (dict(T=65), INVALID, "up to 64"), (dict(T=64, k=9), INVALID, "512"), (dict(T=64, k=1 << 58), INVALID, "512"), (dict(k=0), INVALID, "k ="),
     (dict(E=0), INVALID, "E ="), (dict(E=4097), INVALID, "E ="), (dict(H=24), INVALID, "H ="), (dict(I=0), INVALID, "I ="),
     (dict(I=40), INVALID, "I ="), (dict(mx=1, H=48, g1=None, g2=None), INVALID, "multiples of 32"), (dict(mx=2), INVALID, "mx"),
     (dict(act=0), INVALID, "activation"), (dict(act=3), INVALID, "activation"), (dict(ld_x=100), INVALID, "ld_x"),
@@ -119,6 +120,7 @@ def test_sample_refusals(L, kw, status, needle):
 
 def test_workspace_sizes():
     for f, bad in ((nv.lora_workspace_bytes, (4, 20, 32, 16)), (nv.moe_layer_workspace_bytes, (65, 2, 8, 128, 64)),
+                   (nv.moe_layer_workspace_bytes, (64, 1 << 58, 8, 128, 64)),
                    (nv.sample_workspace_bytes, (4, 0))):
         with pytest.raises(ValueError):
             f(*bad)

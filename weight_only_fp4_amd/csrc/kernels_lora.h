@@ -138,9 +138,8 @@ __device__ __forceinline__ void lora_chunks(const uint16_t* const (&xr)[M], cons
 }
 
 // RT rank tiles of 16, MT tiles of 16 rows at a time (or one, where a list has
-// no more).  Grid: (K slices, places or tiles, shares of a list or
-// turns).  Each wave
-// takes a share of the slice's chunks; the waves' sums meet in LDS.
+// no more).  Grid: (K slices, places or tiles, shares of a list or turns).  Each
+// wave takes a share of the slice's chunks; the waves' sums meet in LDS.
 template <int RT, int MT, bool F16>
 __global__ void __launch_bounds__(kLoraThreads) k_lora_down(LoraArgs a) {
     __shared__ float red[kLoraWaves][MT * kLoraRows * RT * 16];

@@ -192,7 +192,7 @@ __device__ __forceinline__ void sample_values(const uint4& v, F&& f) {
 // The same of one 32-bit word of a piece, e of its first logit in the piece: the
 // loops over words stay loops, because code that runs a few times only costs
 // its fetch (eight logits unrolled in each pass: 64 x 131072 top-p 66 us, one
-// user's 131072 logits without a filter 30; so 57 and 23).
+// user's 131072 logits without a filter 30; so 60 and 24).
 template <int DT, typename F>
 __device__ __forceinline__ void sample_word(uint32_t w, int e, F&& f) {
     if (DT == kLogitF32) f(e, __uint_as_float(w));
@@ -482,9 +482,8 @@ __device__ __forceinline__ int sample_listed_bins(const SampleSettings& set) {
     return set.p < 1.f ? kSampleBins - 1 : sample_min_p_bins(set);
 }
 
-// Grid: (slices, rows).  A thread's pieces are kSampleScanThreads
-// apart; a slice of up to
-// 1024 is read once and stays in LDS.
+// Grid: (slices, rows).  A thread's pieces are kSampleScanThreads apart; a slice
+// of up to 1024 is read once and stays in LDS.
 template <int DT>
 __global__ void __launch_bounds__(kSampleScanThreads) k_sample_scan(SampleArgs a) {
     constexpr int P = Logit<DT>::kPiece;

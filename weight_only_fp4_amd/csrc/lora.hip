@@ -107,6 +107,8 @@ nvfp4_status nvfp4_lora_add(const void* x, int64_t ld_x, const void* a, int64_t 
     if (T == 0 || N == 0) return ok();
     if (ld_x < K || ld_y < N || ld_o < N || ld_x >= kFar || ld_y >= kFar || ld_o >= kFar)
         return fail(NVFP4_ERR_INVALID_ARG, "%s: a leading dimension is below its row's length or too large", fn);
+    if (out == y && T > 1 && ld_o != ld_y)   // rows without an adapter are not copied then
+        return fail(NVFP4_ERR_INVALID_ARG, "%s: out is y with another leading dimension", fn);
     if (a_l < 0 || a_r < 0 || b_l < 0 || b_n < 0 || a_l >= kFar || a_r >= kFar || b_l >= kFar || b_n >= kFar)
         return fail(NVFP4_ERR_INVALID_ARG, "%s: strides of a or b are out of range", fn);
     if (!x || !y || !out || !adapter || (L > 0 && (!a || !b))) return fail(NVFP4_ERR_INVALID_ARG, "%s: NULL pointer", fn);

@@ -39,7 +39,7 @@ FewShape few_shape(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
 }
 
 nvfp4_status sizes(const char* fn, int64_t T, int64_t k, int64_t E, int64_t H, int64_t I, int mx) {
-    if (T < 0 || T > kFewTokens || k < 1 || T * k > kFewPairs)
+    if (T < 0 || T > kFewTokens || k < 1 || k > kFewPairs || T * k > kFewPairs)
         return fail(NVFP4_ERR_INVALID_ARG,
                     "%s: T = %lld, k = %lld: up to %d tokens and %d (token, slot) pairs (more rows go by nvfp4_moe_route, "
                     "nvfp4_moe_fc1, the grouped GEMM and nvfp4_moe_combine)",

@@ -14,8 +14,8 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 constexpr int64_t kMostVocab = (int64_t)1 << 23;   // the steps of a row fit sample_slow's counters
 constexpr int64_t kMostRows = 65535;               // rows are a grid's second axis
 
-// Slices of a row: of 1024 16-byte pieces, which a workgroup holds in registers
-// (4 a thread), or of more where rows are long or so many that 1024 workgroups
+// Slices of a row: of 1024 16-byte pieces, which a workgroup holds in LDS
+// (2 a thread), or of more where rows are long or so many that 1024 workgroups
 // are there without.
 struct SampleShape {
     int S, slice, bits;   // bits: 2^bits logits a slice at most
