@@ -110,7 +110,7 @@ def test_strided_table_and_given_outputs():
     assert (big[:, :4] == 77).all() and (big[:, 4 + table.shape[1]:] == 77).all()
 
 
-@pytest.mark.parametrize("B,most", [(5, 4), (5, 3000)])
+@pytest.mark.parametrize("B,most", [(5, 4), (5, 3000), (32, 32), (41, 25), (65, 3)])
 def test_steps_that_advance_in_place_and_as_a_graph(B, most):
     """lengths over cached and head over free_head: each step goes on where the last ended, also replayed."""
     rng = np.random.default_rng(most)

@@ -32,6 +32,8 @@ def check(got, y, x, a, b, adapter, scale):
     (17, 4096, 257, 64, 5, FP), (33, 520, 1000, 24, 3, BF), (40, 2048, 72, 128, 9, FP), (64, 5120, 640, 32, 64, BF),
     (255, 256, 48, 40, 4, FP), (256, 264, 130, 48, 300, BF), (257, 256, 66, 72, 6, BF), (600, 640, 320, 16, 2, FP),
     (1003, 1152, 31, 104, 1, BF), (16, 16384, 16, 16, 16, BF), (300, 8200, 24, 8, 5, FP),
+    (384, 256, 150, 16, 30, BF), (385, 256, 150, 16, 30, BF), (385, 512, 150, 64, 3, FP), (1100, 136, 264, 128, 77, BF),
+    (2048, 128, 2048, 8, 40, BF),
 ])
 def test_lora(T, K, N, R, L, dtype):
     args = make(T, K, N, R, L, dtype, seed=T + K)

@@ -28,7 +28,8 @@
 // Measured in a graph: 1 token of 128 experts, top-8, 2048 x 768 (21.2 MB of
 // weights): 13.5 us (1.6 TB/s; the chain of latencies is most of it); 16 tokens
 // of it: 47 with NVFP4 weights; 5 tokens of 8 experts, top-2, 4096 x 14336
-// (0.7 GB if each has a pair): 99 (5 to 6 of the 7 TB/s that a plain read reaches).
+// (0.59 GB, six experts, on average): 92 to 101 (6 of the 7 TB/s that a plain read
+// reaches).
 //
 // Waves add into accumulators of their own and are summed in a fixed order, as
 // the splits are: no result depends on timing.

@@ -13,8 +13,9 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 constexpr int64_t kMost = (int64_t)1 << 30;   // requests, rows and tokens of a table's row stay below
 
-// Rows that one workgroup writes alone where an output is an input's memory.
-constexpr int64_t kPlanAlone = 4096;
+// Rows that one workgroup writes alone where an output is an input's memory (16
+// rows: 3.9 us, by two launches 5.5; 1024: 5.8 and 5.9; 4096: 11.2 and 5.9).
+constexpr int64_t kPlanAlone = 1024;
 
 // Whether the call may take two launches, by its sizes alone (the workspace
 // is for them).
@@ -94,8 +95,9 @@ nvfp4_status nvfp4_kv_plan(const int32_t* cached, const int32_t* fresh, int64_t 
     hipStream_t st = static_cast<hipStream_t>(stream);
     const bool in_place = lengths == cached || head_out == head;
     if (B <= kPlanLds && (!in_place || T <= kPlanAlone)) {
-        // few requests: fewer waves to wait for at each barrier
-        if (B <= 64 * kPlanItems && T <= 256) launch_whole<64>(a, in_place, st);
+        // few requests: fewer waves to wait for at each barrier (16 requests 3.9
+        // us with 64 threads, 4.2 with 256; 64: 4.15 and 4.35; 200: 5.4 and 4.7)
+        if (B <= 64 && T <= 256) launch_whole<64>(a, in_place, st);
         else if (B <= 256 * kPlanItems) launch_whole<256>(a, in_place, st);
         else launch_whole<kPlanMaxThreads>(a, in_place, st);
         return launched(fn);

@@ -50,30 +50,38 @@ LoraShape lora_shape(int64_t T, int64_t K, int64_t L) {
 }
 
 // The grid's third axis.  Shares of a list, where adapters have few workgroups
-// otherwise: rows / 64 at most.  Tiles: two turns, so that where one prompt
-// ends and the next begins both adapters go at once.
-unsigned shares(int64_t T, int places, int64_t blocks) {
-    if (!places) return 2;
-    const int64_t want = 1024 / (blocks * places), most = (T + kLoraTile - 1) / kLoraTile;
+// otherwise: rows / 64 at most (512 rows of 8 adapters in lists: 22 us, without
+// shares 27; 133 rows of 12: no difference).  Tiles: two turns, so that where
+// one prompt ends and the next begins both adapters go at once (2048 prompt
+// rows of 6 adapters: 24 us, one turn 27), and up to eight while there are few
+// workgroups (2048 rows of 16 adapters in any order: 47 us, two turns 50).
+unsigned shares(int64_t T, const LoraShape& s, int64_t blocks) {
+    const int64_t want = (s.places ? 1024 : 2048) / (blocks * s.groups);
+    if (!s.places) return (unsigned)(want < 2 ? 2 : want < 8 ? want : 8);
+    const int64_t most = (T + kLoraTile - 1) / kLoraTile;
     return (unsigned)(want < 1 ? 1 : want < most ? want : most);
 }
 
 template <int RT, int MT, bool F16>
 void launch_down(const LoraArgs& a, const LoraShape& s, hipStream_t st) {
-    hipLaunchKernelGGL((k_lora_down<RT, MT, F16>), dim3((unsigned)a.slices, (unsigned)s.groups, shares(a.T, s.places, a.slices)),
+    hipLaunchKernelGGL((k_lora_down<RT, MT, F16>), dim3((unsigned)a.slices, (unsigned)s.groups, shares(a.T, s, a.slices)),
                        dim3(kLoraThreads), 0, st, a);
 }
 template <int KT, bool F16>
 void launch_up(LoraArgs a, const LoraShape& s, hipStream_t st) {
-    // as many columns a wave as leave 512 workgroups (tiles, whose rows are 64: 1024), up to 256
+    // as many columns a wave as leave 512 workgroups (tiles: 1024, but 64 columns
+    // at least), up to 256: B's fragments are asked for once a step of 32, a
+    // list's rows' sums made once a workgroup (133 rows, rank 64: 17.6 us with
+    // 512, 21 with 1024; tiles of 4099 rows: 48.2 with 1024, 50.6 with 512; of
+    // 2048 rows of 16 adapters: 50 with 64 columns, 63 with 32)
     const int64_t enough = s.places ? 512 : 1024;
     int64_t blocks;
     a.cols = 8 * kLoraCols;
     for (;; a.cols /= 2) {
         blocks = (a.N + kLoraWaves * a.cols - 1) / (kLoraWaves * a.cols);
-        if (a.cols == kLoraCols || blocks * s.groups >= enough) break;
+        if (a.cols == (s.places ? kLoraCols : 2 * kLoraCols) || blocks * s.groups >= enough) break;
     }
-    hipLaunchKernelGGL((k_lora_up<KT, F16>), dim3((unsigned)blocks, (unsigned)s.groups, shares(a.T, s.places, blocks)),
+    hipLaunchKernelGGL((k_lora_up<KT, F16>), dim3((unsigned)blocks, (unsigned)s.groups, shares(a.T, s, blocks)),
                        dim3(kLoraThreads), 0, st, a);
 }
 template <bool F16>
