@@ -91,7 +91,8 @@ class DecoderLayer:
         weights, ids = torch.topk(torch.softmax((h @ self.router.t()).float(), -1), self.topk)
         weights = (weights / weights.sum(-1, keepdim=True)).contiguous()
         ids = ids.to(torch.int32)
-        if x.shape[0] <= 64:   # a decoding batch: the whole layer in one call
+        # a decoding batch: the whole layer in one call, which is faster while experts have few rows
+        if x.shape[0] <= 64 and 2 * ids.numel() <= 3 * self.experts:
             return nv.moe_layer(h, ids, weights, self.fc1, self.fc2, self.experts, self.width, self.fc1_scale,
                                 self.fc2_scale), residual
         offsets, row_token, token_row = nv.moe_route(ids, self.experts)

@@ -707,8 +707,9 @@ nvfp4_status nvfp4_lora_add(const void* x, int64_t ld_x, const void* a, int64_t 
  * sums are fp32, and a enters the second product with 16 (bf16) or 22 (fp16)
  * bits (beyond fp16's range as infinity).  Results are bitwise reproducible.  A
  * pair whose id is outside [0, E) adds nothing; a token may name an expert twice.
- * With many rows an expert (T * k above two or three times E) the separate calls
- * can be faster (64 tokens of 128 experts, top-8, 2048 x 768: 128 us here, 96).
+ * With many rows an expert (T * k above one and a half to three times E) the
+ * separate calls are faster (128 experts, top-8, 2048 x 768: 24 tokens 59 us here
+ * and 60 by them, 32 73 and 65, 64 140 and 96).
  *   x [T][ld_x] of H values, topk_ids int32 and topk_weights fp32 [T][k], w_fc1 a
  *   blob of nvfp4_repack_gated (NVFP4_MOE_SILU_GLU) or nvfp4_repack
  *   (NVFP4_MOE_RELU2) of E experts, I and H; w_fc2 of nvfp4_repack (E, H, I);
