@@ -40,11 +40,11 @@ namespace nvfp4 {
 
 constexpr int kFewTokens = 64;
 constexpr int kFewPairs = 512;
-// Pairs of a workgroup of the first product: its rows, four at a time.  An expert
+// Pairs that a workgroup of the first product does at most: its rows.  An expert
 // with more has its weights read again, which the caches answer: 8 or 16 rows
-// cost more in registers and empty rows than they save (64 tokens of 128
-// experts, top-8, 2048 x 768: 128 us with 4, 145 with 8, 174 with 16; 64 of 8,
-// top-2, 4096 x 2048, where each has 16 rows: 94, 88, 95).
+// cost more in registers and empty rows than they save (with a in one part, 64
+// tokens of 128 experts, top-8, 2048 x 768: 128 us with 4, 145 with 8, 174 with
+// 16; 64 of 8, top-2, 4096 x 2048, where each has 16 rows: 94, 88, 95).
 constexpr int kFewRows = 4;
 // Pairs of an item of the second product.  Their two parts are rows of it: one
 // or two pairs take one product of four rows, three or four a second one on the
