@@ -344,10 +344,15 @@ __global__ void __launch_bounds__(kLoraThreads) k_lora_up(LoraArgs a) {
                             o[e] = pack_round2<F16>(sum(in[e] & 0xFFFFu, 2 * e), sum(in[e] >> 16, 2 * e + 1));
                         *reinterpret_cast<uint4*>(orow + n) = make_uint4(o[0], o[1], o[2], o[3]);
                     } else {
+                        // all of y first: out may be its memory, so that loads would stay behind stores
+                        // (60 rows, 4103 columns, rank 128: 5 us more than 4096 columns, 7 that way)
                         const uint16_t* yr = a.y + (int64_t)row[m] * a.ld_y;
+                        uint32_t in[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) in[e] = n + e < a.N ? yr[n + e] : 0u;
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            if (n + e < a.N) orow[n + e] = (uint16_t)round_out<F16>(sum(yr[n + e], e));
+                            if (n + e < a.N) orow[n + e] = (uint16_t)round_out<F16>(sum(in[e], e));
                     }
                 }
             }

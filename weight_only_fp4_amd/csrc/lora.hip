@@ -50,21 +50,22 @@ LoraShape lora_shape(int64_t T, int64_t K, int64_t L) {
 }
 
 // The grid's third axis.  Shares of a list, where adapters have few workgroups
-// otherwise: rows / 64 at most (512 rows of 8 adapters in lists: 22 us, without
-// shares 27; 133 rows of 12: no difference).  Tiles: two turns, so that where
-// one prompt ends and the next begins both adapters go at once (2048 prompt
+// otherwise: up to one for every `rows` rows, which a workgroup takes at a time
+// (60 rows of one adapter of rank 128, 4096 columns: 21 us, 37 with one share for
+// 64 rows; 128 of 4: 23 and 28; 133 rows of 12, rank 64: 17.7 with either).
+// Tiles: two turns, so that where one prompt ends and the next begins both adapters go at once (2048 prompt
 // rows of 6 adapters: 24 us, one turn 27), and up to eight while there are few
 // workgroups (2048 rows of 16 adapters in any order: 47 us, two turns 50).
-unsigned shares(int64_t T, const LoraShape& s, int64_t blocks) {
+unsigned shares(int64_t T, const LoraShape& s, int64_t blocks, int rows) {
     const int64_t want = (s.places ? 1024 : 2048) / (blocks * s.groups);
     if (!s.places) return (unsigned)(want < 2 ? 2 : want < 8 ? want : 8);
-    const int64_t most = (T + kLoraTile - 1) / kLoraTile;
+    const int64_t most = (T + rows - 1) / rows;
     return (unsigned)(want < 1 ? 1 : want < most ? want : most);
 }
 
 template <int RT, int MT, bool F16>
 void launch_down(const LoraArgs& a, const LoraShape& s, hipStream_t st) {
-    hipLaunchKernelGGL((k_lora_down<RT, MT, F16>), dim3((unsigned)a.slices, (unsigned)s.groups, shares(a.T, s, a.slices)),
+    hipLaunchKernelGGL((k_lora_down<RT, MT, F16>), dim3((unsigned)a.slices, (unsigned)s.groups, shares(a.T, s, a.slices, MT * kLoraRows)),
                        dim3(kLoraThreads), 0, st, a);
 }
 template <int KT, bool F16>
@@ -81,7 +82,7 @@ void launch_up(LoraArgs a, const LoraShape& s, hipStream_t st) {
         blocks = (a.N + kLoraWaves * a.cols - 1) / (kLoraWaves * a.cols);
         if (a.cols == (s.places ? kLoraCols : 2 * kLoraCols) || blocks * s.groups >= enough) break;
     }
-    hipLaunchKernelGGL((k_lora_up<KT, F16>), dim3((unsigned)blocks, (unsigned)s.groups, shares(a.T, s, blocks)),
+    hipLaunchKernelGGL((k_lora_up<KT, F16>), dim3((unsigned)blocks, (unsigned)s.groups, shares(a.T, s, blocks, kLoraTile)),
                        dim3(kLoraThreads), 0, st, a);
 }
 template <bool F16>
