@@ -686,7 +686,7 @@ nvfp4_status nvfp4_kv_plan(const int32_t* cached, const int32_t* fresh, int64_t 
  *   with the same leading dimension; no other overlap), a [L] matrices [R][K]
  *   (strides a_l, a_r), b [L] matrices [N][R] (strides b_l, b_n), adapter int32
  *   [T], scale fp32 [L] or NULL for 1.  Rows of x, a and b are 16-byte aligned;
- *   y and out need 2 bytes (16-byte aligned rows are faster).
+ *   y and out need 2 bytes.
  *   workspace: nvfp4_lora_workspace_bytes(T, K, N, R) bytes, 16-byte aligned,
  *   any contents.
  * R a multiple of 8 in [8, 128], K a multiple of 8.  T == 0 or N == 0 launches

@@ -57,7 +57,6 @@ struct LoraArgs {
     int64_t a_l, a_r, b_l, b_n;   // strides of adapters and rows, in values
     int T, K, N, R, L;
     int slices, slice;     // K slices and the values of one (a multiple of 8)
-    int vec;               // rows of y and out are 16-byte aligned
     int cols;              // output columns of a wave, a multiple of kLoraCols
     int places;            // workgroups by adapter: min(L, T); 0: by neighbouring rows
 };
@@ -221,6 +220,20 @@ __device__ __forceinline__ void lora_split(const float (&v)[8], float up, uint4&
     lo = make_uint4(pl[0], pl[1], pl[2], pl[3]);
 }
 
+// Eight values of a row of y or out, whose rows begin anywhere: one access of 16
+// bytes, which global memory takes at any address (8296 rows of 1031 columns: 27
+// us, by two bytes 52; aligned rows as before).
+struct __attribute__((packed, aligned(2))) LoraPiece {
+    uint32_t w[4];
+};
+__device__ __forceinline__ uint4 lora_load(const uint16_t* p) {
+    const LoraPiece v = *reinterpret_cast<const LoraPiece*>(p);
+    return make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+}
+__device__ __forceinline__ void lora_store(uint16_t* p, uint4 v) {
+    *reinterpret_cast<LoraPiece*>(p) = LoraPiece{{v.x, v.y, v.z, v.w}};
+}
+
 // KT steps of 32 ranks.  Grid: (column blocks, places or tiles, shares of a list
 // or turns).  64 rows of a list at a time: their h is added up over the K slices
 // and split, into LDS in the order of the matrix instruction's operand; then a
@@ -263,11 +276,11 @@ __global__ void __launch_bounds__(kLoraThreads) k_lora_up(LoraArgs a) {
                         bv[j][s] = *reinterpret_cast<const uint4*>(br + (rank < a.R ? rank : 0));
                     }
                 }
-                if (a.vec && a.N >= 8) {   // a piece that is not whole: the row's first, not used
+                if (a.N >= 8) {   // a piece that is not whole: the row's first, not used
                     const int from = n0 + 8 * g + 8 <= a.N ? n0 + 8 * g : 0;
 #pragma unroll
                     for (int m = 0; m < kTiles; ++m)
-                        if (m < tiles) yv[m] = *reinterpret_cast<const uint4*>(a.y + (int64_t)row[m] * a.ld_y + from);
+                        if (m < tiles) yv[m] = lora_load(a.y + (int64_t)row[m] * a.ld_y + from);
                 }
             };
             ask(n_first);
@@ -309,7 +322,7 @@ __global__ void __launch_bounds__(kLoraThreads) k_lora_up(LoraArgs a) {
             if (F16 && threadIdx.x < kLoraTile) s_most[threadIdx.x] = 0;
             for (int n0 = n_first; n0 < n_end; n0 += kLoraCols) {
                 const int n = n0 + 8 * g;
-                const bool whole = a.vec && n + 8 <= a.N;
+                const bool whole = n + 8 <= a.N;
                 uint4 b0[2][KT], y0[kTiles];
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
@@ -342,10 +355,9 @@ __global__ void __launch_bounds__(kLoraThreads) k_lora_up(LoraArgs a) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             o[e] = pack_round2<F16>(sum(in[e] & 0xFFFFu, 2 * e), sum(in[e] >> 16, 2 * e + 1));
-                        *reinterpret_cast<uint4*>(orow + n) = make_uint4(o[0], o[1], o[2], o[3]);
+                        lora_store(orow + n, make_uint4(o[0], o[1], o[2], o[3]));
                     } else {
                         // all of y first: out may be its memory, so that loads would stay behind stores
-                        // (60 rows, 4103 columns, rank 128: 5 us more than 4096 columns, 7 that way)
                         const uint16_t* yr = a.y + (int64_t)row[m] * a.ld_y;
                         uint32_t in[8];
 #pragma unroll
@@ -369,8 +381,8 @@ __global__ void __launch_bounds__(kLoraThreads) k_lora_up(LoraArgs a) {
             for (int n = n_first + 8 * (lane & 3); n < n_end; n += kLoraCols) {
                 const uint16_t* yr = a.y + row * a.ld_y + n;
                 uint16_t* orow = a.out + row * a.ld_o + n;
-                if (a.vec && n + 8 <= a.N) {
-                    *reinterpret_cast<uint4*>(orow) = *reinterpret_cast<const uint4*>(yr);
+                if (n + 8 <= a.N) {
+                    lora_store(orow, lora_load(yr));
                 } else {
                     for (int e = 0; e < 8; ++e)
                         if (n + e < a.N) orow[e] = yr[e];

@@ -53,9 +53,10 @@ LoraShape lora_shape(int64_t T, int64_t K, int64_t L) {
 // otherwise: up to one for every `rows` rows, which a workgroup takes at a time
 // (60 rows of one adapter of rank 128, 4096 columns: 21 us, 37 with one share for
 // 64 rows; 128 of 4: 23 and 28; 133 rows of 12, rank 64: 17.7 with either).
-// Tiles: two turns, so that where one prompt ends and the next begins both adapters go at once (2048 prompt
-// rows of 6 adapters: 24 us, one turn 27), and up to eight while there are few
-// workgroups (2048 rows of 16 adapters in any order: 47 us, two turns 50).
+// Tiles: two turns, so that where one prompt ends and the next begins both
+// adapters go at once (2048 prompt rows of 6 adapters: 24 us, one turn 27), and up
+// to eight while there are few workgroups (2048 rows of 16 adapters in any order:
+// 47 us, two turns 50).
 unsigned shares(int64_t T, const LoraShape& s, int64_t blocks, int rows) {
     const int64_t want = (s.places ? 1024 : 2048) / (blocks * s.groups);
     if (!s.places) return (unsigned)(want < 2 ? 2 : want < 8 ? want : 8);
@@ -156,7 +157,6 @@ nvfp4_status nvfp4_lora_add(const void* x, int64_t ld_x, const void* a, int64_t 
     g.slices = s.slices;
     g.slice = s.slice;
     g.places = s.places;
-    g.vec = aligned(y, 16) && aligned(out, 16) && ld_y % 8 == 0 && ld_o % 8 == 0;
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (f16) launch<true>(g, s, st);
     else launch<false>(g, s, st);
