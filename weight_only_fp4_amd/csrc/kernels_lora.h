@@ -32,8 +32,8 @@ constexpr int kLoraTile = 64;        // neighbouring rows of a workgroup
 // Rows up to which a workgroup belongs to an adapter.  Lists against tiles, us,
 // 4096 x 4096: 256 rows of 16 adapters in any order 15, 18; 300 of 32 14, 26; 300
 // of 3 prompts 13, 14; 512 of 8 adapters in any order 22, 13; 1000 of 16 30, 27;
-// 1000 of 4 prompts 29, 16.
-constexpr int kLoraLists = 384;
+// 1000 of 4 prompts 29, 16; 4096 x 2421, 361 rows of one of 40 adapters 64, 20.
+constexpr int kLoraLists = 256;
 constexpr int kLoraThreads = 256;
 constexpr int kLoraWaves = kLoraThreads / 64;
 constexpr int kLoraMaxRank = 128;
