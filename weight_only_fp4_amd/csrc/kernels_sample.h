@@ -477,6 +477,13 @@ __device__ __forceinline__ float sample_bin(float l, float grid) { return floorf
 // Whether the bins near the largest logit's are exact (products to a quarter of
 // a bin) and finite; rows where they are not take sample_slow.
 __device__ __forceinline__ bool sample_grid_holds(float largest, float grid) { return fabsf(largest) * grid < 4194304.f; }
+// The same of a slice's largest, which may lie up to the bins' whole reach
+// further from zero than that of a row that holds: every slice such a row counts
+// has to have added its weights.  (Products are then off by a quarter of a bin
+// at most, as sample_min_p_bins allows; a bin is one for all slices either way.)
+__device__ __forceinline__ bool sample_grid_reaches(float largest, float grid) {
+    return fabsf(largest) * grid < 4194304.f + 2 * kSampleBins;
+}
 // Bins below the largest that min-p may keep: one more for the grid's place, one for its rounding.
 __device__ __forceinline__ int sample_min_p_bins(const SampleSettings& set) {
     if (!set.filters) return kSampleBins - 1;
@@ -559,7 +566,7 @@ __global__ void __launch_bounds__(kSampleScanThreads) k_sample_scan(SampleArgs a
             const float d = top - sample_bin(l, grid);
             if (d < (float)kSampleBins) atomicAdd(reinterpret_cast<uint32_t*>(&s_bins[(int)d]), 1u);
         });
-    } else if (sample_grid_holds(largest, grid)) {   // the largest is finite: its weight comes out as 1 by itself
+    } else if (sample_grid_reaches(largest, grid)) {   // the largest is finite: its weight comes out as 1 by itself
         const SampleWeights sw(largest, set.t, a.slice_shift);
         all([&](int, float l) {
             const float d = top - sample_bin(l, grid);
