@@ -704,12 +704,14 @@ nvfp4_status nvfp4_lora_add(const void* x, int64_t ld_x, const void* a, int64_t 
  * X' = RNE16(x * pre_scale1) if that is given (pre_scale1 [H], pre_scale2 [I]).
  * Unlike the separate calls (nvfp4_moe_fc1, the grouped GEMM, nvfp4_moe_combine),
  * which round h, a and the experts' outputs to 16 bits, nothing is on the way:
- * sums are fp32, and a enters the second product with 16 (bf16) or 22 (fp16)
- * bits (beyond fp16's range as infinity).  Results are bitwise reproducible.  A
- * pair whose id is outside [0, E) adds nothing; a token may name an expert twice.
- * With many rows an expert (T * k above one and a half to three times E) the
- * separate calls are faster (128 experts, top-8, 2048 x 768: 24 tokens 59 us here
- * and 60 by them, 32 73 and 65, 64 140 and 96).
+ * sums are fp32, and a enters the second product with fp32's range and 24 bits
+ * (below 2^-110 with fewer).  Results are bitwise reproducible; a token's last
+ * bits may depend on the other tokens' number and experts, which decide where
+ * sums are cut.  A pair whose id is outside [0, E) adds nothing; a token may name
+ * an expert twice.
+ * With many rows an expert the separate calls are faster (128 experts, top-8,
+ * 2048 x 768: 16 tokens 46 us here and 49 by them, 24 60 and 60, 32 74 and 64, 64
+ * 147 and 88; 8 experts, top-2, 4096 x 14336: 1 token 44 and 48, 5 100 and 92).
  *   x [T][ld_x] of H values, topk_ids int32 and topk_weights fp32 [T][k], w_fc1 a
  *   blob of nvfp4_repack_gated (NVFP4_MOE_SILU_GLU) or nvfp4_repack
  *   (NVFP4_MOE_RELU2) of E experts, I and H; w_fc2 of nvfp4_repack (E, H, I);

@@ -5,10 +5,15 @@
 //   out_t = RNE16(sum_j w_tj g2_e (a_p W2_e^T))                    k_moe_few_fc2
 //
 // X' with the first pre-quant scale applied (RNE16) where given.  Sums stay fp32
-// from x to out; a is handed on as two 16-bit parts, the rounded value and what
-// the rounding took off, each a row of the second product (16 bits in bf16, 22
-// in fp16: with the rounded value alone the layer's error was 1.4 to 1.55 times
-// that of rounding the output; 16 tokens took 45 us for 47).
+// from x to out, and a is handed on whole: as three bf16 parts of 8 bits, which
+// are multiplied one after another into the same sums.  In both types: bf16 has
+// fp32's range, and bare E2M1 values are exact in it.  (Below 2^-110 the last part
+// is a bf16 denormal or nothing.)  Two parts of the layer's own type were 16 bits
+// in bf16, 22 in fp16 for values near one only, and none beyond 65504; 1 / 16 / 5
+// wide tokens (as below) took 13.9 / 49.5 / 104 us.  Tried for three: a row of the
+// product for each part, items of two pairs 14.1 / 53.8 / 120, of four 15.8 / 59 /
+// 118 (registers spill); two fp16 parts with a power of two for every 16 values
+// 15.4 / 56 / 119 (two more loads a chunk).
 //
 // Both kernels contract as the small-M GEMM does (kernels_gemm.h) and read
 // each active expert's weights once for every four of its rows.  What
@@ -25,14 +30,16 @@
 // no exchange of rows: it is formed where the products are, and split workgroups
 // exchange 16 columns of T rows.
 //
-// Measured in a graph: 1 token of 128 experts, top-8, 2048 x 768 (21.2 MB of
-// weights): 13.5 us (1.6 TB/s; the chain of latencies is most of it); 16 tokens
-// of it: 47 with NVFP4 weights; 5 tokens of 8 experts, top-2, 4096 x 14336
-// (0.59 GB, six experts, on average): 92 to 101 (6 of the 7 TB/s that a plain read
-// reaches).
+// Measured in a graph, over sets of inputs beyond the last cache: 1 token of 128
+// experts, top-8, 2048 x 768 (21.2 MB of weights): 13.7 us (1.5 TB/s; the chain of
+// latencies is most of it); 16 tokens of it: 51 with NVFP4 weights (4.0 TB/s); 5
+// tokens of 8 experts, top-2, 4096 x 14336 (0.6 GB, six experts, on average): 110
+// (5.5 of the 7 TB/s that a plain read reaches).
 //
 // Waves add into accumulators of their own and are summed in a fixed order, as
-// the splits are: no result depends on timing.
+// the splits are: no result depends on timing.  Where a token's sum is cut depends
+// on the number of pairs and of items, so its last bits may on the other tokens'
+// experts.
 #pragma once
 #include "kernels_gemm.h"
 
@@ -46,19 +53,17 @@ constexpr int kFewPairs = 512;
 // tokens of 128 experts, top-8, 2048 x 768: 128 us with 4, 145 with 8, 174 with
 // 16; 64 of 8, top-2, 4096 x 2048, where each has 16 rows: 94, 88, 95).
 constexpr int kFewRows = 4;
-// Pairs of an item of the second product.  Their two parts are rows of it: one
-// or two pairs take one product of four rows, three or four a second one on the
-// same decoded weights (items of two pairs only: 12.9 / 48.6 / 100.4 and, 64
-// tokens of 128 experts, 146; so 13.5 / 47.2 / 99.4 and 140; the parts as two
-// products of four pairs' rows: 13.1 / 47.6 / 100.2 and 140).
+// Pairs of an item of the second product, a row of the matrix instruction each.
 constexpr int kFewItem = 4;
+constexpr int kFewParts = 3;
 // Shapes (us of the layer in a graph: 1 token of 128 experts, top-8, 2048 x 768;
 // 16 tokens of it; 5 tokens of 8 experts, top-2, 4096 x 14336):
 //   FC1, waves and depth of their rings: 4 and 2 13.6 / 40.8 / 89.1; 4 and 4 13.7
 //   / 44.2 / 90.5; 2 and 4 14.8 / 41.5 / 87.4; 1 and 4 15.5 / 43.2 / 87.0; 8 and 2
 //   13.8 / 49.0 / 93.2 (with a in one part);
-//   FC2: 8 and 2 13.5 / 47.2 / 99.4; 8 and 3 17.3 / 51.3 / 102.7 (more than 128
-//   registers: one workgroup a compute unit); 4 and 2 14.0 / 49.3 / 100.0.
+//   FC2: 8 and 2 13.7 / 51.4 / 110; 8 and 3 17.2 / 54.2 / 112 (more than 128
+//   registers: one workgroup a compute unit); 4 and 2 14.2 / 51.1 / 110, and 64
+//   tokens of 4 experts, top-1, 26.5 for 24.5.
 constexpr int kFewWaves1 = 4, kFewDepth1 = 2;
 constexpr int kFewWaves = 8, kFewDepth = 2;
 
@@ -84,7 +89,7 @@ struct FewArgs {
     const float* g2;
     const uint16_t* pre1;
     const uint16_t* pre2;
-    uint16_t* a;          // [P][2][I] workspace: the rounded values, the rests
+    uint16_t* a;          // [kFewParts][P][KC2 * 128] workspace: bf16 parts of a, zeros behind I
     FewList* list;        // workspace
     uint16_t* out;
     int64_t ld_o;
@@ -153,6 +158,18 @@ __device__ __forceinline__ void few_list(const FewArgs& f, int32_t* ids, int32_t
     if (tid == 0) f.list->items = items;
 }
 
+// v as three bf16 values whose sum it is, `stride` apart: its upper 8 bits, the 8
+// after them, the last 8.  (An fp32 value less its own upper part is exact.)
+__device__ __forceinline__ void few_split(float v, uint16_t* to, int64_t stride) {
+    const bool finite = fabsf(v) < __builtin_inff();
+#pragma unroll
+    for (int part = 0; part < kFewParts; ++part) {
+        const uint32_t bits = __float_as_uint(v);
+        to[part * stride] = v != v ? (uint16_t)0x7FC0u : (uint16_t)(bits >> 16);
+        v = finite ? v - __uint_as_float(bits & 0xFFFF0000u) : 0.f;   // an infinity or NaN leaves nothing over
+    }
+}
+
 // Grid: (units of W1 / NT, pairs + 1).  NT = 2 with the gate (a pair of units: gate, up).
 template <bool F16, bool PRE, int ACT>
 __global__ void __launch_bounds__(kFewWaves1 * 64) k_moe_few_fc1(FewArgs f) {
@@ -216,17 +233,50 @@ __global__ void __launch_bounds__(kFewWaves1 * 64) k_moe_few_fc1(FewArgs f) {
         float v = ACT == kActSiluGlu ? silu_times(gv * s0, gv * s1) : relu_squared(gv * s0);
         if (n < f.I) {
             if (f.pre2) v = fp32_value(v * act_to_f32<F16>(f.pre2[n]));
-            const uint32_t hi = round_out<F16>(v);
-            const float rest = v - act_to_f32<F16>(hi);   // an infinity (or NaN) leaves nothing over
-            uint16_t* to = f.a + (int64_t)pairs[r] * 2 * f.I + n;
-            to[0] = (uint16_t)hi;
-            to[f.I] = (uint16_t)round_out<F16>(fabsf(rest) < __builtin_inff() ? rest : 0.f);
+            const int64_t row = f.KC2 * kChunkK;
+            uint16_t* to = f.a + pairs[r] * row + n;
+            few_split(v, to, f.P * row);
+            if ((int)blockIdx.x * 16 + 16 == f.I)   // the last columns' workgroup: zeros to the chunk's end
+                for (int past = 16; n + past < row; past += 16) few_split(0.f, to + past, f.P * row);
         }
     }
 }
 
+// What a wave of k_moe_few_fc2 has on its way of a chunk.
+struct FewSlot {
+    uint4 cw, xa[kFewParts];
+    uint32_t sw;
+};
+
+// One chunk of an item: the small-M GEMM's contraction (kernels_gemm.h) with a's
+// parts one after another into the same sums.  The weights enter as bare E2M1
+// values, their scales multiply the sums of 16 columns.
+__device__ __forceinline__ void few_chunk(const FewSlot& s, const float* lut, int lane, f32x4& acc) {
+    const uint32_t sp = scale_pair(s.sw, lane);
+    const float s0 = lut[sp & 0xFFu], s1 = lut[(sp >> 8) & 0xFFu];
+    const s16x4 b0 = decode4_pow2<false, 0>(s.cw.x, 1.f), b1 = decode4_pow2<false, 2>(s.cw.x, 1.f);
+    const s16x4 b2 = decode4_pow2<false, 0>(s.cw.y, 1.f), b3 = decode4_pow2<false, 2>(s.cw.y, 1.f);
+    const s16x4 b4 = decode4_pow2<false, 0>(s.cw.z, 1.f), b5 = decode4_pow2<false, 2>(s.cw.z, 1.f);
+    const s16x4 b6 = decode4_pow2<false, 0>(s.cw.w, 1.f), b7 = decode4_pow2<false, 2>(s.cw.w, 1.f);
+    f32x4 p = {0.f, 0.f, 0.f, 0.f}, r = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int part = kFewParts - 1; part >= 0; --part) {   // the smallest first
+        const s16x4 lo = dwords_to_s16x4(s.xa[part].x, s.xa[part].y), hi = dwords_to_s16x4(s.xa[part].z, s.xa[part].w);
+        p = mma4<false, 2, 0>(lo, b0, p);
+        r = mma4<false, 2, 2>(lo, b4, r);
+        p = mma4<false, 2, 0>(hi, b1, p);
+        r = mma4<false, 2, 2>(hi, b5, r);
+        p = mma4<false, 2, 1>(lo, b2, p);
+        r = mma4<false, 2, 3>(lo, b6, r);
+        p = mma4<false, 2, 1>(hi, b3, p);
+        r = mma4<false, 2, 3>(hi, b7, r);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(s1, r[i], __builtin_fmaf(s0, p[i], acc[i]));
+}
+
 struct FewShared {
-    float2 lut[256];
+    float lut[256];   // the weights' scales
     FewItem item[kFewPairs];
     int32_t pair[kFewPairs];
     float weight[kFewPairs];
@@ -250,7 +300,7 @@ __global__ void __launch_bounds__(kFewWaves * 64) k_moe_few_fc2(FewArgs f) {
         sh.pair[i] = f.list->pair[i];
         sh.weight[i] = f.list->weight[i];
     }
-    build_scale_table(sh.lut, f.w2.mx);
+    for (int b = tid; b < 256; b += kThreads) sh.lut[b] = f.w2.mx ? e8m0_to_f32((uint32_t)b) : e4m3_to_f32((uint32_t)b);
     for (int i = tid; i < kFewWaves * out_n; i += kThreads) sums[i] = 0.f;
     __syncthreads();
 
@@ -266,24 +316,20 @@ __global__ void __launch_bounds__(kFewWaves * 64) k_moe_few_fc2(FewArgs f) {
         At ld = {(int)(lo / f.KC2), (int)(lo % f.KC2)}, us = ld;
         int64_t ld_i = 0;
         const uint8_t *codes = nullptr, *scales = nullptr;   // the load side's unit
-        uint32_t row[2];   // the byte offsets of this lane's activation rows: pairs 0 and 1, 2 and 3
+        uint32_t row = 0;   // the byte offset of this lane's piece of its pair's row
         auto enter = [&]() {   // the load side's item
             const int e = __builtin_amdgcn_readfirstlane(sh.item[ld.item].e);
             const int first = sh.item[ld.item].first, rows = sh.item[ld.item].rows;
             const int64_t blk = f.w2.block(e, u, 0);
             codes = f.w2.codes + blk * kCodeBlock;
             scales = f.w2.scales + blk * kScaleBlock;
-            // row ai of a group of four: part ai & 1 of its pair ai >> 1
-#pragma unroll
-            for (int mg = 0; mg < 2; ++mg) {
-                const int at = 2 * mg + (ai >> 1);
-                row[mg] = (uint32_t)((2 * sh.pair[first + (at < rows ? at : 0)] + (ai & 1)) * (int64_t)f.I * 2);
-            }
+            row = (uint32_t)(sh.pair[first + (ai < rows ? ai : 0)] * f.KC2 * kChunkK + kpiece) * 2;
         };
         enter();
-        f32x4 acc[1][2] = {{f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}}};
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
         const uint8_t* ab = reinterpret_cast<const uint8_t*>(f.a);
-        auto load = [&](SmallSlot<2, 1>& slot, int64_t i) {
+        const int64_t part_bytes = (int64_t)f.P * f.KC2 * kChunkK * 2;
+        auto load = [&](FewSlot& slot, int64_t i) {
             if (i > ld_i) {   // i is the last one, or one more
                 ld_i = i;
                 if (++ld.chunk == f.KC2) {
@@ -293,26 +339,15 @@ __global__ void __launch_bounds__(kFewWaves * 64) k_moe_few_fc2(FewArgs f) {
                 }
             }
             const int64_t off = (int64_t)ld.chunk * f.w2.chunk_stride;
-            slot.cw[0] = load_stream_u4(codes + off * kCodeBlock + (uint32_t)(lane * 16));
-            slot.sw[0] = load_scale_dword(scales + off * kScaleBlock, lane);
-            const int kk = ld.chunk * kChunkK + kpiece;
-            const uint32_t kb = kk < f.I ? (uint32_t)(kk * 2) : 0u;
+            slot.cw = load_stream_u4(codes + off * kCodeBlock + (uint32_t)(lane * 16));
+            slot.sw = load_scale_dword(scales + off * kScaleBlock, lane);
+            const uint8_t* ac = ab + ld.chunk * (kChunkK * 2);
 #pragma unroll
-            for (int mg = 0; mg < 2; ++mg) slot.xa[mg] = *reinterpret_cast<const uint4*>(ab + (row[mg] + kb));
+            for (int part = 0; part < kFewParts; ++part)
+                slot.xa[part] = *reinterpret_cast<const uint4*>(ac + part * part_bytes + row);
         };
-        auto use = [&](const SmallSlot<2, 1>& slot, int64_t i) {
-            const bool kin = us.chunk * kChunkK + kpiece < f.I;
-            if (sh.item[us.item].rows > 2) {
-                small_m_chunk<2, 1, false, F16, false>(slot, kin, sh.lut, lane, acc);
-            } else {
-                SmallSlot<1, 1> half;
-                half.cw[0] = slot.cw[0];
-                half.sw[0] = slot.sw[0];
-                half.xa[0] = slot.xa[0];
-                f32x4 one[1][1] = {{acc[0][0]}};
-                small_m_chunk<1, 1, false, F16, false>(half, kin, sh.lut, lane, one);
-                acc[0][0] = one[0][0];
-            }
+        auto use = [&](const FewSlot& slot, int64_t i) {
+            few_chunk(slot, sh.lut, lane, acc);
             const bool ends = us.chunk == f.KC2 - 1;
             if (ends || i == n - 1) {
                 // the item's rows into the tokens' sums: lane l < 16 has column l
@@ -320,7 +355,7 @@ __global__ void __launch_bounds__(kFewWaves * 64) k_moe_few_fc2(FewArgs f) {
                 const float gv = sh.item[us.item].g;
 #pragma unroll
                 for (int r = 0; r < kFewItem; ++r) {
-                    float v = acc[0][r >> 1][2 * r & 3] + acc[0][r >> 1][(2 * r & 3) + 1];
+                    float v = acc[r];
                     v += __shfl_xor(v, 16);
                     v += __shfl_xor(v, 32);
                     if (lane < 16 && r < rows) {
@@ -328,12 +363,12 @@ __global__ void __launch_bounds__(kFewWaves * 64) k_moe_few_fc2(FewArgs f) {
                         *to = __builtin_fmaf(sh.weight[first + r] * gv, v, *to);
                     }
                 }
-                acc[0][0] = acc[0][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+                acc = f32x4{0.f, 0.f, 0.f, 0.f};
             }
             if (ends) ++us.item, us.chunk = 0;
             else ++us.chunk;
         };
-        SmallSlot<2, 1> ring[kFewDepth];
+        FewSlot ring[kFewDepth];
         const int64_t last = n - 1;
 #pragma unroll
         for (int d = 0; d < kFewDepth; ++d) {

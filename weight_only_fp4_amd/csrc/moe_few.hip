@@ -12,7 +12,7 @@ namespace {
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 constexpr int64_t kFewCounters = NVFP4_MOE_LAYER_COUNTER_BYTES / 4;   // units whose columns may be split
-constexpr int64_t kFewLd = (int64_t)1 << 21;                          // offsets of 512 rows in two parts fit 32 bits
+constexpr int64_t kFewLd = (int64_t)1 << 21;                          // offsets of a part's 512 rows fit 32 bits
 
 struct FewShape {
     int S;
@@ -32,7 +32,7 @@ FewShape few_shape(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
     if (S > 16) S = 16;
     s.S = S < 1 ? 1 : (int)S;
     s.a_at = NVFP4_MOE_LAYER_COUNTER_BYTES;
-    s.list_at = s.a_at + round_up(P * I * 4, 256);
+    s.list_at = s.a_at + P * KC * kChunkK * kFewParts * 2;
     s.part_at = s.list_at + round_up((int64_t)sizeof(FewList), 256);
     s.total = s.part_at + (s.S > 1 ? (int64_t)s.S * NU * T * kUnitN * 4 : 0);
     return s;

@@ -76,7 +76,7 @@ def moe_layer(x, topk_ids, topk_weights, w1, w2, E, I, g1=None, g2=None, divisor
     """The whole expert layer of up to 64 tokens (512 (token, slot) pairs) in two launches: x [T, H] bf16 or fp16,
     topk_ids int32 and topk_weights fp32 [T, k] (ids outside [0, E) add nothing), w1 from ``repack_gated`` (MOE_SILU_GLU)
     or ``repack`` (MOE_RELU2), w2 from ``repack``, g1 and g2 fp32 [E]; mxfp4: blobs of the MXFP4 repacks and no g1, g2.
-    pre_scale1 [H], pre_scale2 [I]: the products' pre-quant scales.  Nothing but the output is rounded to 16 bits.
+    pre_scale1 [H], pre_scale2 [I]: the products' pre-quant scales.  Nothing else is rounded to 16 bits than X' and the output.
     workspace_buf: ``workspace(moe_layer_workspace_bytes(...), device)``, reusable by moe_layer calls of any sizes on one
     stream; made per call if not given.  More tokens: ``moe_route``, ``moe_fc1``, ``grouped_gemm``, ``moe_combine``."""
     return (_attention._binding or _attention._native()).moe_layer(x, topk_ids, topk_weights, w1, w2, E, I, g1, g2,
