@@ -680,8 +680,11 @@ nvfp4_status nvfp4_kv_plan(const int32_t* cached, const int32_t* fresh, int64_t 
 /* Low-rank adapters beside a shared projection: with a = adapter[t],
  *   out[t] = RNE16(y[t] + scale[a] * (x[t] A_a^T) B_a^T),
  * or y[t] unchanged where a is outside [0, L).  Sums are fp32; x A_a^T enters
- * the second product with 16 (bf16) or 22 (fp16) bits, in two parts, so that an
- * infinite value of B gives an infinity or NaN.
+ * the second product with 16 (bf16) or 22 (fp16) bits, in two parts (in fp16 on a
+ * scale of its row: values below 2^-16 of the row's largest have fewer), so that
+ * an infinite value of B gives an infinity or NaN.  A row depends on no other
+ * row's values or adapter; where its sum over K is cut depends on T, K and L, so
+ * the last bits may differ between calls of different sizes.
  *   x [T][ld_x] of K values, y and out [T][ld_y], [T][ld_o] of N (out may be y
  *   with the same leading dimension; no other overlap), a [L] matrices [R][K]
  *   (strides a_l, a_r), b [L] matrices [N][R] (strides b_l, b_n), adapter int32
@@ -689,8 +692,10 @@ nvfp4_status nvfp4_kv_plan(const int32_t* cached, const int32_t* fresh, int64_t 
  *   y and out need 2 bytes.
  *   workspace: nvfp4_lora_workspace_bytes(T, K, N, R) bytes, 16-byte aligned,
  *   any contents.
- * R a multiple of 8 in [8, 128], K a multiple of 8.  T == 0 or N == 0 launches
- * nothing.  Errors: sizes (T <= 1048560, K and N < 2^24), NULL pointers ->
+ * R a multiple of 8 in [8, 128], K a multiple of 8 (rows of a and b in 16-byte
+ * pieces): a lower rank is padded, once, with rows of zeros in a and columns of
+ * zeros in b, a higher one goes in parts (out as the next call's y, which rounds
+ * it).  T == 0 or N == 0 launches nothing.  Errors: sizes (T <= 1048560, K and N < 2^24), NULL pointers ->
  * INVALID_ARG; misaligned -> ALIGNMENT; workspace too small -> BUFFER_TOO_SMALL. */
 int64_t nvfp4_lora_workspace_bytes(int64_t T, int64_t K, int64_t N, int64_t R); /* < 0 if invalid */
 nvfp4_status nvfp4_lora_add(const void* x, int64_t ld_x, const void* a, int64_t a_l, int64_t a_r, const void* b, int64_t b_l,

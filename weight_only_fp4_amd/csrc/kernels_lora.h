@@ -29,10 +29,15 @@ namespace nvfp4 {
 
 constexpr int kLoraRows = 16;        // rows of a product
 constexpr int kLoraTile = 64;        // neighbouring rows of a workgroup
-// Rows up to which a workgroup belongs to an adapter.  Lists against tiles, us,
-// 4096 x 4096: 256 rows of 16 adapters in any order 15, 18; 300 of 32 14, 26; 300
-// of 3 prompts 13, 14; 512 of 8 adapters in any order 22, 13; 1000 of 16 30, 27;
-// 1000 of 4 prompts 29, 16; 4096 x 2421, 361 rows of one of 40 adapters 64, 20.
+// Rows up to which a workgroup belongs to an adapter.  T and L alone do not say
+// how the rows are spread (that is on the device), and each form loses where the
+// other wins.  Lists against tiles, us, 4096 x 4096, rank 16: 256 rows of one of 40
+// adapters 29, 14; of 32 in any order 13, 26; 300 of 32 in any order 14, 26; of 3
+// prompts 13, 14; 512 of 8 in any order 22, 13; 1000 of 16 30, 27; 1000 of 4
+// prompts 29, 16; 361 rows of one of 40, 2421 columns, 64, 20.  Lists end where
+// their worst case has grown to four times the other's and tiles' stays at twice:
+// rows of one adapter have a workgroup for all of them in lists, rows in any order
+// a turn for each adapter in tiles.
 constexpr int kLoraLists = 256;
 constexpr int kLoraThreads = 256;
 constexpr int kLoraWaves = kLoraThreads / 64;
