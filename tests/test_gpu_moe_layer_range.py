@@ -135,3 +135,21 @@ def test_infinite_and_nan_activations(dtype):
     rows = torch.tensor([0, 1, 3], device=DEV)
     assert torch.isnan(got[2]).all() and torch.isfinite(got[rows]).all()
     check(layer, got[rows], x[rows], ids[rows], w[rows])
+
+
+@pytest.mark.parametrize("T,k,E,H,I", [(1, 1, 1, 16, 16), (3, 2, 4, 64, 16), (5, 1, 2, 48, 144), (9, 3, 4, 1040, 272),
+                                       (64, 8, 9, 32, 112)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_rows_that_end_inside_a_chunk(T, k, E, H, I, dtype):
+    """What lies behind a row of a in the workspace counts for nothing: it was NaN, and is what other calls left."""
+    layer = Layer(E, H, I, dtype, seed=T)
+    x, ids, w = layer.tokens(T, k)
+    ws = torch.full((nv.moe_layer_workspace_bytes(64, 8, E, H, 512),), 255, dtype=torch.uint8, device=DEV)
+    ws[:4096] = 0
+    want = layer.run(x, ids, w, workspace_buf=ws)
+    check(layer, want, x, ids, w)
+    big = Layer(E, H, 512, dtype, seed=1)
+    bx, bids, bw = big.tokens(64, min(8, k + 1))
+    bx[:] = float("inf")
+    big.run(bx, bids, bw, workspace_buf=ws)
+    assert torch.equal(layer.run(x, ids, w, workspace_buf=ws), want)

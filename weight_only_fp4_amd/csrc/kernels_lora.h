@@ -15,10 +15,11 @@
 // their adapter) it belongs to 64 neighbouring rows and takes the adapters that
 // occur among them one after another.
 //
-// Measured in a graph, the two kernels' own times behind: 16 tokens of 32
-// adapters, 4096 x 4096, rank 16 8.3 us (3.4 + 5.1); 133 tokens of 12, 4096 x
-// 14336, rank 64 18.0 (6.3 + 11.5; 37 MB, 2.0 TB/s); 4099 rows of 6 prompts, 5120
-// x 5120, rank 32 44 to 48 (16.7, 2.6 TB/s, + 28.2, 3.0 TB/s).
+// Measured in a graph over sets of inputs beyond the last cache, the two kernels'
+// own times behind: 16 tokens of 32 adapters, 4096 x 4096, rank 16 8.5 us (4.0 +
+// 5.3); 133 tokens of 12, 4096 x 14336, rank 64 20.5 (7.3 + 13.7; 37 MB, 1.8
+// TB/s); 4099 rows of 6 prompts, 5120 x 5120, rank 32 49 (20.3, 2.1 TB/s, + 29.8,
+// 2.8 TB/s).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>

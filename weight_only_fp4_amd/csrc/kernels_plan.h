@@ -19,8 +19,8 @@
 // costs less than the second launch that sharing them would.  Where an output
 // is an input's memory only one workgroup may run, or a launch for the scans and
 // one for the rows (k_plan, k_plan_rows); the latter also for more requests.
-// Measured in a graph: 16 requests of a token each 4.4 us, 257 with 16384 rows
-// 7.9, 600 prompts with 131072 rows 8.3 (1.7 MB: 0.2 TB/s).
+// Measured in a graph: 16 requests of a token each 3.9 us, 257 with 16384 rows
+// 7.5, 600 prompts with 131072 rows 7.8 (1.7 MB: 0.2 TB/s).
 // Sums are 32 bits wide and saturate above all limits (T, F < 2^30), divisions
 // by the page size are multiplications.
 #pragma once

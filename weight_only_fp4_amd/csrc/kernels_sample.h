@@ -33,10 +33,11 @@
 // of 8 bits a round finds each threshold.
 //
 // What bounds it is no rate of the memory (64 x 131072 bf16 logits are 2.4 us)
-// but fp64 exponentials and LDS additions in the slices and a chain of some
-// twenty barriers a row.  Measured in a graph, scan + pick: 1 x 131072, top-k 50
-// 20.5 us (6.8 + 13.4); 23 x 32003 fp32, min-p 22.0 (5.8 + 17.2); 64 x 131072,
-// top-p 59.7 (18.2 + 41.2).  One workgroup a row in one launch took 250, 31, 370.
+// but the slices' fp64 exponentials (64 x 131072: 8 of 19 us, behind which the
+// additions in LDS hide) and a chain of some twenty barriers a row.  Measured in a
+// graph, scan + pick: 1 x 131072, top-k 50 20.3 us (7.2 + 13.4); 23 x 32003 fp32,
+// min-p 23.5 (6.3 + 16.6); 64 x 131072, top-p 59.8 (19.4 + 41.6).  One workgroup a
+// row in one launch took 250, 31, 370; rows that take sample_slow 210 to 430.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
