@@ -55,9 +55,11 @@ def parse():
     return p.parse_args()
 
 
-# The attention half's sources: no workload here runs them.
+# The sources of the attention half and of what a decode step runs around its layers: no workload here runs them.
 NOT_TIMED = {"attn.hip", "attn_plan.h", "binding.cpp", "kernels_attn.h", "kernels_kv.h", "kernels_norm.h",
-             "nvfp4_attention.hip", "quant.h"}
+             "nvfp4_attention.hip", "quant.h",
+             "binding_step.h", "kernels_lora.h", "kernels_moe_few.h", "kernels_plan.h", "kernels_sample.h", "kv_plan.hip",
+             "lora.hip", "moe_few.hip", "sample.hip"}
 
 
 def source_digest() -> str:
